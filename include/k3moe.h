@@ -572,6 +572,152 @@ k3_status k3_moe_layer_cached(const uint16_t *x, const uint16_t *router_w,
                               int32_t *idx, float *w, double *logits, void *ws,
                               size_t ws_bytes, k3_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key/value cache: the attention half of a decoding step, with drafted
+ * trees. One step of a batch of R requests runs k3_kv_plan once, then for
+ * each layer k3_qk_norm_rope (norm, rotation, append) and k3_tree_attention,
+ * and, once the drafts are judged, k3_kv_commit over all layers.
+ *
+ * Terms. Request r has ctx[r] committed tokens in the cache and new[r] tokens
+ * in this step (one token, a prompt's chunk, or the nodes of a drafted tree
+ * whose parents are given). The step's T tokens lie one request after
+ * another: token t = cu[r] + i is node i of request r and has the place
+ * ctx[r] + i in the request's cache. A place p is in page table[r][p / P],
+ * slot p % P, P = page_size; its slot number is page * P + p % P.
+ *
+ * All integer arrays are int32 on the device, dense, 4-byte aligned; rows of
+ * keys, values and queries are 16-byte aligned. What the device finds in the
+ * arrays cannot be refused on the host: each call says what it does with
+ * lengths, pages and parents out of range, and none reads or writes outside
+ * the buffers that its arguments describe.
+ * T = 0 is a step without tokens: accepted, and the per-token arrays may
+ * then be NULL.
+ *
+ * k3_kv_cache describes one layer's cache: element [page][slot][head][d] of
+ * the keys is at k + page * page_stride + slot * slot_stride + head *
+ * head_stride + d (strides in elements, every row's byte offset a multiple
+ * of 16), the values alike. 16-bit caches hold the model's type and have no
+ * scales; an e4m3 cache holds x / scale[head], saturated at +-448, with fp32
+ * scales [n_heads] on the device (NULL: 1). n_pages * page_size < 2^31;
+ * byte offsets may pass 32 bits; a table's row has at most 2^30
+ * places (blocks * page_size). head_dim is 64, 128 or 256.
+ * ---------------------------------------------------------------------- */
+#define K3_BF16 0
+#define K3_F16 1
+#define K3_E4M3 2
+#define K3_MAX_REQUESTS 4096
+#define K3_MAX_TREE_WORDS 32
+#define K3_MAX_ACCEPTED 1024
+#define K3_MAX_HEADS 1024
+
+typedef struct k3_kv_cache {
+  void *k, *v;
+  const float *k_scale, *v_scale;
+  int64_t page_stride, slot_stride, head_stride;
+  int32_t n_pages, page_size, n_heads, head_dim;
+  int32_t dtype;
+} k3_kv_cache;
+
+/* The plan of a step. Request r needs ceil((ctx + new) / P) pages and holds
+ * held[r], the first held[r] entries of its row of table [R][blocks]. Missing
+ * pages are taken, in the requests' order, from the ring of free pages (ring
+ * [n_pages]; ring_state = {place of the first free page, number of free
+ * pages}) and entered in the table; pages that it no longer needs are put at
+ * the ring's end (a request that has ended: ctx = new = 0). A request whose
+ * missing pages, with those of the requests before it, are more than the free
+ * ones is not served: it keeps what it holds, kv_lens[r] = 0 and its slots
+ * are -1. So is one with a length that is negative or past the table's row,
+ * held[r] outside [0, blocks], more nodes than the mask has bits, or more
+ * pages to give back than the ring has room for (it asks for none and gives
+ * none). `table` and `ring` are updated in place;
+ * the others are outputs apart from the inputs:
+ *   held_out [R], ring_out [2]  the new held and ring_state
+ *   cu [R + 1]                  prefix sums of new (negative ones count as
+ *                               0; sums stop at 2^30)
+ *   kv_lens [R]                 ctx + new, 0 if not served
+ *   slots, positions [T]        slot numbers (-1: not served, or a page id
+ *                               outside [0, n_pages)); rotary positions
+ *                               ctx + i, or ctx + depth in the tree (at
+ *                               most 2^31 - 1)
+ *   mask [T][words]             with parents: bit j of row t says that node
+ *                               j is t's node or an ancestor of it
+ *   status [2]                  requests not served; tokens past T (sum of
+ *                               new - T, at least 0), for which nothing is
+ *                               written
+ * Tokens in [cu[R], T) (a padded step) get slot -1, position 0, mask 0.
+ * parents [T] (NULL: no trees; then mask is not written): the index of a
+ * node's parent among its request's nodes, in any order; the root, and any
+ * index outside the request, has no parent. A cycle ends where it closes.
+ * R in [1, K3_MAX_REQUESTS], words in [1, K3_MAX_TREE_WORDS] with parents. */
+k3_status k3_kv_plan(const int32_t *ctx, const int32_t *new_, const int32_t *parents,
+                     int R, int T, int n_pages, int page_size, int blocks,
+                     const int32_t *held, int32_t *ring, const int32_t *ring_state,
+                     int32_t *table, int32_t *held_out, int32_t *ring_out,
+                     int32_t *cu, int32_t *kv_lens, int32_t *slots,
+                     int32_t *positions, int32_t *mask, int words,
+                     int32_t *status, k3_stream_t stream);
+
+/* Norm of queries and keys for each head, rotation, and the append, in one
+ * pass: y = x * rsqrt(mean(x^2) + eps) * w, then the pairs (a, b) of the
+ * first `rot` values become (a cos - b sin, b cos + a sin) for the angle
+ * positions[t] * inv_freq[i], i < rot / 2: a, b are values i and i + rot / 2,
+ * or 2i and 2i + 1 if `interleaved`. Rotated queries go to q_out; rotated
+ * keys and the values as they are go to the cache rows at slots[t] (rows with
+ * a slot outside [0, n_pages * P) are not written; two tokens with one slot
+ * leave either). fp32 throughout, angles in fp64, one rounding at the end.
+ * q_in [T][Hq][D], k_in and v_in [T][n_heads][D] with token strides in
+ * elements (multiples of 8) and dense heads, q_out likewise; dtype K3_BF16 or
+ * K3_F16 for all of them and wq, wk [D]. The cache holds dtype or e4m3.
+ * inv_freq fp32 [rot / 2]; rot a multiple of 16, 0 <= rot <= D (0: no
+ * rotation, inv_freq may be NULL). */
+k3_status k3_qk_norm_rope(const void *q_in, int64_t q_stride, const void *k_in,
+                          int64_t k_stride, const void *v_in, int64_t v_stride,
+                          int dtype, int T, int Hq, const void *wq, const void *wk,
+                          float eps, const float *inv_freq, int rot,
+                          int interleaved, const int32_t *positions, void *q_out,
+                          int64_t q_out_stride, const k3_kv_cache *cache,
+                          const int32_t *slots, k3_stream_t stream);
+
+/* Attention of the step's tokens over the paged cache. With L = kv_lens[r],
+ * n = cu[r + 1] - cu[r], query head hq of node i reads key head
+ * hq / (Hq / n_heads) at the places j < L; places below L - n are seen by
+ * every node, place L - n + j' by node i if bit j' of mask row cu[r] + i is
+ * set (mask [T][words]; bits past the words are 0), or, with mask NULL, if
+ * j' <= i. out = sum_j softmax_j(scale * q . k_j) v_j over the places seen;
+ * lse (optional, fp32 [T][Hq]) = log sum_j exp(scale * q . k_j). A row that
+ * sees nothing has out 0 and lse -inf. What lies at places not seen, NaN and
+ * infinities too, changes nothing. Places in a page outside [0, n_pages) are
+ * not seen; a request with kv_lens below 0 or past the table's row sees
+ * nothing. A request whose cu is not ascending
+ * within [0, T] is left out, and so are the rows of tokens past cu[R].
+ * q and out [T][Hq][D] of dtype K3_BF16 or K3_F16 with token strides
+ * in elements (multiples of 8); the cache holds dtype or e4m3. Scores, the
+ * softmax's maximum and sum and the output's sum are fp32; the weights are
+ * rounded to dtype for the product with the values. Results do not depend on
+ * timing: the same call gives the same bits. Needs a workspace of
+ * k3_tree_attention_workspace_bytes(T, Hq, n_heads, head_dim) bytes (0 for
+ * shapes it does not support). */
+size_t k3_tree_attention_workspace_bytes(int T, int Hq, int n_heads, int head_dim);
+k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T,
+                            int Hq, const k3_kv_cache *cache, const int32_t *table,
+                            int blocks, const int32_t *cu, const int32_t *kv_lens,
+                            int R, const int32_t *mask, int words, float scale,
+                            void *out, int64_t out_stride, void *ws,
+                            size_t ws_bytes, float *lse, k3_stream_t stream);
+
+/* Keeps the accepted path of each request's tree, in every layer: the rows
+ * at the places ctx[r] + accepted[r][i], i < n_accepted[r], move to ctx[r] +
+ * i, keys and values, as if all were read before any is written; ctx_out[r]
+ * = ctx[r] + n_accepted[r]. accepted [R][most]: node indices in strictly
+ * ascending order. Layer l's cache is at cache->k + l * layer_stride (and v
+ * alike, elements). A request with n_accepted outside [0, most], indices
+ * that do not ascend from >= 0, or a row to move whose place has no page,
+ * stays as it is, with ctx_out[r] = ctx[r]. ctx_out is apart from ctx. */
+k3_status k3_kv_commit(const k3_kv_cache *cache, int layers, int64_t layer_stride,
+                       const int32_t *table, int blocks, const int32_t *ctx,
+                       const int32_t *accepted, const int32_t *n_accepted,
+                       int most, int R, int32_t *ctx_out, k3_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

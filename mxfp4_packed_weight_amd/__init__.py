@@ -21,9 +21,11 @@ _lib = None
 K3_OK, K3_ERR_ARG, K3_ERR_CONFIG, K3_ERR_MEMORY, K3_ERR_DEVICE = 0, 1, 2, 3, 4
 K3_MAX_EXPERTS, K3_MAX_TOPK, K3_MAX_SHARED = 4096, 64, 8
 K3_WAIT_LIMIT_DEFAULT = 1 << 20
+K3_BF16, K3_F16, K3_E4M3 = 0, 1, 2
+K3_MAX_REQUESTS, K3_MAX_TREE_WORDS, K3_MAX_ACCEPTED, K3_MAX_HEADS = 4096, 32, 1024, 1024
 
 # (name, restype, argtypes) of every exported symbol in include/k3moe.h
-_vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_vp, _i, _sz, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
 
 
 class k3_cache_stats(ctypes.Structure):
@@ -32,6 +34,15 @@ class k3_cache_stats(ctypes.Structure):
 
     def as_dict(self):
         return {f: int(getattr(self, f)) for f, _ in self._fields_}
+
+
+class k3_kv_cache(ctypes.Structure):
+    """One layer's paged cache as the C calls take it; k3_kv_cache_of fills it
+    from tensors and keeps them alive."""
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("k", "v", "k_scale", "v_scale")]
+                + [(f, ctypes.c_int64) for f in ("page_stride", "slot_stride", "head_stride")]
+                + [(f, ctypes.c_int32) for f in ("n_pages", "page_size", "n_heads", "head_dim",
+                                                 "dtype")])
 
 
 _stats_p = ctypes.POINTER(k3_cache_stats)
@@ -102,6 +113,13 @@ SIGNATURES = [
                                              _vp, _vp, _vp, _sz, _vp]),
     ("k3_moe_layer_cached", _i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp,
                                  _vp, _sz, _vp]),
+    ("k3_kv_plan", _i, [_vp] * 3 + [_i] * 5 + [_vp] * 11 + [_i, _vp, _vp]),
+    ("k3_qk_norm_rope", _i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _i, _i, _vp, _vp,
+                             ctypes.c_float, _vp, _i, _i, _vp, _vp, _i64, _vp, _vp, _vp]),
+    ("k3_tree_attention_workspace_bytes", _sz, [_i, _i, _i, _i]),
+    ("k3_tree_attention", _i, [_vp, _i64, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _i, _vp, _i,
+                               ctypes.c_float, _vp, _i64, _vp, _sz, _vp, _vp]),
+    ("k3_kv_commit", _i, [_vp, _i, _i64, _vp, _i, _vp, _vp, _vp, _i, _i, _vp, _vp]),
 ]
 
 
@@ -491,3 +509,91 @@ def k3_moe_layer_from_logits_cached(X, logits, bias, cache, n_experts, hidden, i
     _call("k3_moe_layer_from_logits_cached", _dp(X), _dp(logits), _dp(bias), _vp(cache),
           n_experts, hidden, inter, k, T, _dp(Y), _dp(Y_f32), _dp(idx), _dp(w), _dp(ws),
           _nbytes(ws), _stream(stream))
+
+
+# ---- paged key/value cache --------------------------------------------------
+# Tensors only (strides and types are read off them); a cache is the handle
+# that k3_kv_cache_of returns, made once per layer.
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _kv_dtype(t):
+    import torch
+    codes = {torch.bfloat16: K3_BF16, torch.float16: K3_F16, torch.float8_e4m3fn: K3_E4M3}
+    if t.dtype not in codes:
+        raise TypeError(f"bfloat16, float16 or float8_e4m3fn, not {t.dtype}")
+    return codes[t.dtype]
+
+
+def _heads(name, t, dtype, D):
+    """Token stride of rows [T, heads, D] or [T, heads * D] with dense heads."""
+    if _kv_dtype(t) != dtype:
+        raise TypeError(f"{name} is {t.dtype}, not the type of the call's other rows")
+    dense = t.dim() in (2, 3) and t.stride(-1) == 1
+    if dense and t.dim() == 3:
+        dense = t.shape[2] == D and (t.shape[1] == 1 or t.stride(1) == D)
+    if not dense:
+        raise ValueError(f"{name}: rows [T, heads, {D}] with dense heads, "
+                         f"not {tuple(t.shape)} with strides {t.stride()}")
+    return t.stride(0)
+
+
+def k3_kv_cache_of(k, v, k_scale=None, v_scale=None):
+    """The handle of one layer's cache: k, v [pages, page_size, heads, D]
+    views in any order in memory with dense rows; fp32 scales [heads] for
+    float8_e4m3fn caches (None: 1)."""
+    import torch
+    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+        raise ValueError("k and v: [pages, page_size, heads, D], alike in shape, strides and type")
+    if k.stride(3) != 1:
+        raise ValueError(f"rows of keys and values are dense, not of stride {k.stride(3)}")
+    for s in (k_scale, v_scale):
+        if s is not None and (s.dtype != torch.float32 or s.numel() != k.shape[2]
+                              or not s.is_contiguous()):
+            raise ValueError("scales are float32 [heads]")
+    c = k3_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.stride(0), k.stride(1),
+                    k.stride(2), k.shape[0], k.shape[1], k.shape[2], k.shape[3], _kv_dtype(k))
+    c.tensors = (k, v, k_scale, v_scale)
+    return c
+
+
+def k3_kv_plan(ctx, new, parents, R, T, n_pages, page_size, blocks, held, ring, ring_state, table,
+               held_out, ring_out, cu, kv_lens, slots, positions, mask, words, status,
+               stream=None):
+    _call("k3_kv_plan", _ptr(ctx), _ptr(new), _ptr(parents), R, T, n_pages, page_size, blocks,
+          _ptr(held), _ptr(ring), _ptr(ring_state), _ptr(table), _ptr(held_out), _ptr(ring_out),
+          _ptr(cu), _ptr(kv_lens), _ptr(slots), _ptr(positions), _ptr(mask), words, _ptr(status),
+          _stream(stream))
+
+
+def k3_qk_norm_rope(q_in, k_in, v_in, T, Hq, wq, wk, eps, inv_freq, rot, interleaved, positions,
+                    q_out, cache, slots, stream=None):
+    dt, D = _kv_dtype(q_in), cache.head_dim
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w.dtype != q_in.dtype:
+            raise TypeError(f"{name} is {w.dtype}, not the type of the call's rows")
+    _call("k3_qk_norm_rope", _ptr(q_in), _heads("q_in", q_in, dt, D), _ptr(k_in),
+          _heads("k_in", k_in, dt, D), _ptr(v_in), _heads("v_in", v_in, dt, D), dt, T, Hq,
+          _ptr(wq), _ptr(wk), eps, _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(positions),
+          _ptr(q_out), _heads("q_out", q_out, dt, D), ctypes.byref(cache), _ptr(slots),
+          _stream(stream))
+
+
+def k3_tree_attention_workspace_bytes(T, Hq, n_heads, head_dim):
+    return lib().k3_tree_attention_workspace_bytes(T, Hq, n_heads, head_dim)
+
+
+def k3_tree_attention(q, T, Hq, cache, table, blocks, cu, kv_lens, R, mask, words, scale, out, ws,
+                      lse=None, stream=None):
+    dt, D = _kv_dtype(q), cache.head_dim
+    _call("k3_tree_attention", _ptr(q), _heads("q", q, dt, D), dt, T, Hq, ctypes.byref(cache),
+          _ptr(table), blocks, _ptr(cu), _ptr(kv_lens), R, _ptr(mask), words, scale, _ptr(out),
+          _heads("out", out, dt, D), _ptr(ws), _nbytes(ws), _ptr(lse), _stream(stream))
+
+
+def k3_kv_commit(cache, layers, layer_stride, table, blocks, ctx, accepted, n_accepted, most, R,
+                 ctx_out, stream=None):
+    _call("k3_kv_commit", ctypes.byref(cache), layers, layer_stride, _ptr(table), blocks,
+          _ptr(ctx), _ptr(accepted), _ptr(n_accepted), most, R, _ptr(ctx_out), _stream(stream))
