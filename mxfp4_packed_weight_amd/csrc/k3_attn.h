@@ -4,15 +4,16 @@
 // Rows. The G query heads of a key head and a request's n nodes are n * G
 // rows that read the same keys; row = node * G + head. A tile is RT of them.
 //
-// Division of the work. A unit is one tile times one block of KB keys; the
-// units of a call stand in one line (request, key head, tile, block), and
-// each of B workgroups takes an equal stretch of it, whatever the requests'
-// lengths. A tile whose blocks fall to several workgroups leaves partial
-// results (sum of weighted values, maximum, sum), at most two per workgroup:
-// slot 0 for a tile that began before its stretch, slot 1 for one that goes
-// on after it. A second launch joins them in the line's order. The lengths
-// are on the device, so every workgroup works the line out for itself: one
-// prefix sum over the requests.
+// Division of the work. The tiles of a call stand in one line (request, key
+// head, tile), each as long as the places that its rows may see, and each of
+// B workgroups takes an equal stretch of the line, in whole blocks of KB
+// places, whatever the requests' lengths. A tile whose blocks fall to several
+// workgroups leaves partial results (sum of weighted values, maximum, sum), at
+// most two per workgroup: slot 0 for a tile that began before its stretch,
+// slot 1 for one that goes on after it. A second launch joins them in the
+// line's order. The lengths are on the device, so every workgroup works the
+// line out for itself: one prefix sum over the requests, and a closed form
+// within each.
 #pragma once
 
 #include <math.h>
@@ -30,6 +31,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
+constexpr int kMaxWorkgroups = 1024;  // of a launch: at most two to a CU
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The running maximum is raised only by more than this (in powers of two):
 // weights up to 2^8 are exact as ever in fp32 and bf16, and the output is
@@ -40,7 +42,7 @@ constexpr float kSlack = 8.f;
 template <bool BF>
 constexpr float kLift = BF ? 0.f : 6.f;
 
-// ---- the line of units ----------------------------------------------------
+// ---- the line ---------------------------------------------------------------
 
 struct Request {
   int t0, n, len;  // first token, nodes, places
@@ -54,30 +56,37 @@ __device__ __forceinline__ Request request_of(const AttnArgs &a, int r) {
   if (q.len < 0 || q.len > a.blocks * a.c.page_size) q.len = 0;
   return q;
 }
-template <int RT>
-__device__ __forceinline__ int tiles_of(const AttnArgs &a, int n) {
-  return (int)(((long long)n * a.G + RT - 1) / RT);
-}
-template <int KB>
-__device__ __forceinline__ int blocks_of(int len) {
-  return len > 0 ? (len - 1) / KB + 1 : 1;
-}
-template <int RT, int KB>
-__device__ __forceinline__ long long units_of(const AttnArgs &a, int r) {
-  const Request q = request_of(a, r);
-  return (long long)tiles_of<RT>(a, q.n) * a.c.n_heads * blocks_of<KB>(q.len);
-}
 
-// pre[r] = units before request r, pre[R] = all of them; a workgroup of
+// The cost of a request's tiles, in sixteenths of a place: the first tile's,
+// and what each next one has more. T * Hq <= 2^30 rows and 2^30 places keep
+// all sums below 2^61.
+template <int RT, int KB>
+struct Cost {
+  int tiles;
+  long long base, slope;
+  static constexpr long long kFixed = 16 * KB;  // queries in, results out
+  __device__ __forceinline__ Cost(const AttnArgs &a, const Request &q) {
+    tiles = (int)(((long long)q.n * a.G + RT - 1) / RT);
+    const bool causal = !a.mask && q.len >= q.n;
+    slope = causal ? 16 * RT / a.G : 0;
+    base = kFixed + 16ll * (causal ? q.len - q.n : q.len) + slope;
+  }
+  // of the first x tiles of a key head, of tile x
+  __device__ __forceinline__ long long of_first(long long x) const { return x * base + slope * (x * (x - 1) / 2); }
+  __device__ __forceinline__ long long of(int x) const { return base + slope * x; }
+  __device__ __forceinline__ long long of_request(const AttnArgs &a) const { return of_first(tiles) * a.c.n_heads; }
+};
+
+// pre[r] = cost before request r, pre[R] = all of it; a workgroup of
 // THREADS threads. Ends with a barrier.
 template <int RT, int KB, int THREADS>
-__device__ __forceinline__ void line_of_units(const AttnArgs &a, long long *pre) {
+__device__ __forceinline__ void line_of_tiles(const AttnArgs &a, long long *pre) {
   const int tid = threadIdx.x, lane = tid & 63;
   __shared__ long long wave_sum[THREADS / 64];
   if (a.R == 1) {
     if (tid == 0) {
       pre[0] = 0;
-      pre[1] = units_of<RT, KB>(a, 0);
+      pre[1] = Cost<RT, KB>(a, request_of(a, 0)).of_request(a);
     }
     __syncthreads();
     return;
@@ -87,7 +96,7 @@ __device__ __forceinline__ void line_of_units(const AttnArgs &a, long long *pre)
   long long own = 0;
   for (int r = lo; r < hi; r++) {
     pre[r] = own;
-    own += units_of<RT, KB>(a, r);
+    own += Cost<RT, KB>(a, request_of(a, r)).of_request(a);
   }
   long long incl = own;
 #pragma unroll
@@ -104,7 +113,7 @@ __device__ __forceinline__ void line_of_units(const AttnArgs &a, long long *pre)
   __syncthreads();
 }
 
-// The request that unit u belongs to: the last r with pre[r] <= u.
+// The request that place u of the line belongs to: the last r with pre[r] <= u.
 __device__ __forceinline__ int request_at(const long long *pre, int R, long long u) {
   int lo = 0, hi = R - 1;
   while (lo < hi) {
@@ -118,29 +127,62 @@ __device__ __forceinline__ int request_at(const long long *pre, int R, long long
 // A tile in the line.
 struct Tile {
   Request q;
-  int r, h, row0, blocks;
-  long long first;  // its first unit
+  int r, h, row0;
+  int places, blocks;      // that its rows may see: the first `places`, in `blocks` blocks
+  long long first, after;  // its stretch of the line
 };
 template <int RT, int KB>
 __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const long long *pre, long long u) {
   Tile t;
   t.r = request_at(pre, a.R, u);
   t.q = request_of(a, t.r);
-  t.blocks = blocks_of<KB>(t.q.len);
-  const long long x = u - pre[t.r];
-  const long long tile = x / t.blocks;
-  t.first = pre[t.r] + tile * t.blocks;
-  const int tiles = tiles_of<RT>(a, t.q.n);
-  t.h = (int)(tile / tiles);
-  t.row0 = (int)(tile - (long long)t.h * tiles) * RT;
+  const Cost<RT, KB> cost(a, t.q);
+  const long long x = u - pre[t.r], head = cost.of_first(cost.tiles);
+  t.h = (int)(x / head);
+  const long long in_head = x - t.h * head;
+  int lo = 0, hi = cost.tiles - 1;  // the last tile that begins at or before it
+  while (lo < hi) {
+    const int mid = lo + ((hi - lo + 1) >> 1);
+    if (cost.of_first(mid) <= in_head) lo = mid;
+    else hi = mid - 1;
+  }
+  t.row0 = lo * RT;
+  t.first = pre[t.r] + t.h * head + cost.of_first(lo);
+  t.after = t.first + cost.of(lo);
+  t.places = t.q.len;
+  if (!a.mask) {
+    const long long rows = (long long)t.q.n * a.G;
+    const int last = (int)((min(rows, (long long)t.row0 + RT) - 1) / a.G);
+    t.places = min(t.q.len, max(0, t.q.len - t.q.n + last + 1));
+  }
+  t.blocks = t.places > 0 ? (t.places - 1) / KB + 1 : 1;
   return t;
 }
 
-__device__ __forceinline__ long long stretch(long long units, int b, int B) { return units * b / B; }
+// The tile's first block that is done after place u of the line.
+template <int KB>
+__device__ __forceinline__ int block_from(const Tile &t, long long u) {
+  if (u <= t.first) return 0;
+  if (u >= t.after) return t.blocks;
+  const long long y = max(u - t.first - Cost<16, KB>::kFixed, 0ll);
+  return (int)min((y + 16 * KB - 1) / (16 * KB), (long long)t.blocks);
+}
+
+// Where workgroup b's stretch of the line begins.
+struct Stretches {
+  long long each;
+  uint32_t rest, B;
+  __device__ __forceinline__ Stretches(long long cost, int B) : each(cost / B), rest((uint32_t)(cost % B)), B(B) {}
+  __device__ __forceinline__ long long begin(int b) const { return each * b + rest * (uint32_t)b / B; }
+};
+// Neighbours in the line read the same keys: they go to one die (workgroups
+// go to the eight dies in turn, and each has an L2 of its own).
+__device__ __forceinline__ int place_in_line(int b, int B) { return B % 8 ? b : (b & 7) * (B / 8) + (b >> 3); }
 
 // ---- partial results --------------------------------------------------------
 
-// part: for 2 B slots [RT][D] sums, then for each slot [RT] maxima, [RT] sums.
+// part: for 2 B slots [RT][D] sums, then for each slot [RT] maxima, [RT] sums,
+// then B jobs of the joining launch.
 template <int RT, int D>
 __device__ __forceinline__ float *part_o(const AttnArgs &a, int slot, int row) {
   return a.part + ((size_t)slot * RT + row) * D;
@@ -149,7 +191,50 @@ template <int RT, int D>
 __device__ __forceinline__ float *part_ml(const AttnArgs &a, int B, int slot) {
   return a.part + (size_t)2 * B * RT * D + (size_t)slot * 2 * RT;
 }
-inline size_t part_bytes(int RT, int D, int B) { return (size_t)2 * B * RT * (D + 2) * sizeof(float); }
+// What workgroup b leaves to be joined: the tile that began in its stretch and
+// goes on up to workgroup `last`'s (rows = 0: none). Slots are -1 where it had
+// no block.
+struct JoinJob {
+  int t0, h, row0, rows, last;
+  int tail_slot, head_slot;  // its own part of that tile; of a tile from before its stretch
+  int pad;
+};
+template <int RT, int D>
+__device__ __forceinline__ JoinJob *join_jobs(const AttnArgs &a, int B) {
+  return (JoinJob *)(a.part + (size_t)2 * B * RT * (D + 2));
+}
+inline size_t part_bytes(int RT, int D, int B) {
+  return (size_t)2 * B * RT * (D + 2) * sizeof(float) + kMaxWorkgroups * sizeof(JoinJob);
+}
+
+// The walk of a workgroup over its stretch of the line, with
+// segment(tile, first block, block after the last, slot or -1).
+template <int RT, int KB, int D, int THREADS, class Segment>
+__device__ __forceinline__ void walk(const AttnArgs &a, long long *pre, Segment &&segment) {
+  line_of_tiles<RT, KB, THREADS>(a, pre);
+  const int B = gridDim.x, b = place_in_line(blockIdx.x, B);
+  const Stretches line(pre[a.R], B);
+  const long long begin = line.begin(b), end = line.begin(b + 1);
+  JoinJob job = {0, 0, 0, 0, -1, -1, -1, 0};
+  for (long long u = begin; u < end;) {
+    const Tile tile = tile_at<RT, KB>(a, pre, u);
+    const int lo = block_from<KB>(tile, u), hi = block_from<KB>(tile, end);
+    const int slot = lo == hi || (lo == 0 && hi == tile.blocks) ? -1 : lo ? 2 * b : 2 * b + 1;
+    if (u > tile.first) job.head_slot = slot;
+    else if (tile.after > end) {
+      job.t0 = tile.q.t0;
+      job.h = tile.h;
+      job.row0 = tile.row0;
+      job.rows = min(RT, tile.q.n * a.G - tile.row0);
+      job.tail_slot = slot;
+      job.last = b;
+      while (job.last + 1 < B && line.begin(job.last + 1) < tile.after) job.last++;
+    }
+    if (lo < hi) segment(tile, lo, hi, slot);
+    u = tile.after;
+  }
+  if (threadIdx.x == 0) join_jobs<RT, D>(a, B)[b] = job;
+}
 
 // ---- numbers ----------------------------------------------------------------
 

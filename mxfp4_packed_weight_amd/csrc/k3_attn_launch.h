@@ -1,19 +1,33 @@
 // Which attention kernel a call takes, and its launches.
 #pragma once
 
+#include "k3_attn_join.h"
 #include "k3_attn_stream.h"
+#include "k3_attn_tile.h"
 
 namespace k3 {
 
+template <bool BF, int D, int RT>
+hipError_t launch_join(const AttnArgs &a, int B, hipStream_t s) {
+  if (const hipError_t e = hipGetLastError()) return e;
+  attn_join_kernel<BF, D, RT><<<dim3(B, RT < 128 ? RT / kJoinWaves : RT / (2 * kJoinWaves)), 64 * kJoinWaves, 0, s>>>(a, B);
+  return hipGetLastError();
+}
+
 template <bool BF, bool F8, int D, int QT>
 hipError_t launch_stream(const AttnArgs &a, hipStream_t s) {
-  constexpr int RT = 16 * QT;
-  const int B = attn_workgroups();
+  const int B = attn_workgroups(16 * QT);
   const size_t pre = (a.R + 1) * sizeof(long long);
   attn_stream_kernel<BF, F8, D, QT><<<B, kStreamThreads, pre, s>>>(a);
-  if (const hipError_t e = hipGetLastError()) return e;
-  attn_join_kernel<BF, D, RT, kStreamKeys><<<dim3(B, RT / 4), 256, pre, s>>>(a, B);
-  return hipGetLastError();
+  return launch_join<BF, D, 16 * QT>(a, B, s);
+}
+
+template <bool BF, bool F8, int D, int NW>
+hipError_t launch_tile(const AttnArgs &a, hipStream_t s) {
+  const int B = attn_workgroups(32 * NW);
+  const size_t pre = (a.R + 1) * sizeof(long long);
+  attn_tile_kernel<BF, F8, D, NW><<<B, 64 * NW, pre, s>>>(a);
+  return launch_join<BF, D, 32 * NW>(a, B, s);
 }
 
 template <bool BF, bool F8, int D>
@@ -21,9 +35,11 @@ hipError_t launch_attn(const AttnArgs &a, hipStream_t s) {
   switch (attn_tile_rows(a.T, a.G, a.R, D)) {
     case 16: return launch_stream<BF, F8, D, 1>(a, s);
     case 32: return launch_stream<BF, F8, D, 2>(a, s);
-    default:
+    case 64:
       if constexpr (D < 256) return launch_stream<BF, F8, D, 4>(a, s);
       return hipErrorInvalidValue;
+    case 128: return launch_tile<BF, F8, D, 4>(a, s);
+    default: return launch_tile<BF, F8, D, 8>(a, s);
   }
 }
 

@@ -318,7 +318,7 @@ struct Stream {
     const char *v = (const char *)a.c.v + tile.h * a.c.head_stride * ES;
     const int32_t *table = a.table + (size_t)tile.r * a.blocks;
     int64_t *offset = L.offset[wave];
-    const int end = (int)min((long long)hi * kStreamKeys, (long long)rq.len);
+    const int end = (int)min((long long)hi * kStreamKeys, (long long)tile.places);
     int k0 = lo * kStreamKeys + 32 * wave;
     int page = table_entry(a, table, k0 + (lane & 31), rq.len);
     if (k0 < end) {
@@ -409,61 +409,9 @@ __global__ __launch_bounds__(kStreamThreads) void attn_stream_kernel(AttnArgs a)
   using S = Stream<BF, F8, D, QT>;
   extern __shared__ long long pre[];
   __shared__ typename S::Lds L;
-  line_of_units<S::RT, kStreamKeys, kStreamThreads>(a, pre);
-  const int B = gridDim.x, b = blockIdx.x;
-  const long long units = pre[a.R], end = stretch(units, b + 1, B);
-  for (long long u = stretch(units, b, B); u < end;) {
-    const Tile tile = tile_at<S::RT, kStreamKeys>(a, pre, u);
-    const int lo = (int)(u - tile.first), hi = (int)min((long long)tile.blocks, end - tile.first);
-    const int slot = lo ? 2 * b : hi < tile.blocks ? 2 * b + 1 : -1;
-    S::segment(a, L, tile, lo, hi, slot, B);
-    u = tile.first + hi;
-  }
-}
-
-// Joins the tiles that were split: the tile that begins in workgroup b's
-// stretch and goes on in the next ones; a wave per row.
-template <bool BF, int D, int RT, int KB>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int B) {
-  extern __shared__ long long pre[];
-  line_of_units<RT, KB, 256>(a, pre);
-  const int b = blockIdx.x, lane = threadIdx.x & 63;
-  const long long units = pre[a.R], begin = stretch(units, b, B), end = stretch(units, b + 1, B);
-  if (begin == end || end == units) return;
-  const Tile tile = tile_at<RT, KB>(a, pre, end - 1);
-  const long long over = tile.first + tile.blocks;
-  if (tile.first < begin || over <= end) return;
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 6), row = tile.row0 + r;
-  if (row >= tile.q.n * a.G) return;
-  int last = b;  // the workgroup that ends the tile
-  while (stretch(units, last + 1, B) < over) last++;
-  constexpr int N = D / 64;
-  float ref = -INFINITY;
-  for (int x = b + lane; x <= last; x += 64)
-    if (stretch(units, x, B) < stretch(units, x + 1, B))
-      ref = fmaxf(ref, part_ml<RT, D>(a, B, x == b ? 2 * b + 1 : 2 * x)[r]);
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) ref = fmaxf(ref, __shfl_xor(ref, m));
-  float sum = 0.f, o[N];
-#pragma unroll
-  for (int i = 0; i < N; i++) o[i] = 0.f;
-#pragma unroll 4
-  for (int x = b; x <= last; x++) {
-    if (stretch(units, x, B) == stretch(units, x + 1, B)) continue;
-    const int slot = x == b ? 2 * b + 1 : 2 * x;
-    const float *ml = part_ml<RT, D>(a, B, slot), *p = part_o<RT, D>(a, slot, r);
-    const float f = ml[r] == ref ? 1.f : exp2_hw(ml[r] - ref);
-    sum = fmaf(ml[RT + r], f, sum);
-#pragma unroll
-    for (int i = 0; i < N; i++) o[i] = fmaf(p[lane + 64 * i], f, o[i]);
-  }
-  const int i = row / a.G, hq = tile.h * a.G + row - i * a.G;
-  const size_t tok = tile.q.t0 + i;
-  const float f = sum == 0.f ? 0.f : (a.c.v_scale ? a.c.v_scale[tile.h] : 1.f) / sum;
-#pragma unroll
-  for (int j = 0; j < N; j++)
-    a.out[tok * a.out_stride + hq * D + lane + 64 * j] = (uint16_t)pack2<BF>(o[j] * f, 0.f);
-  if (a.lse && lane == 0) a.lse[tok * a.Hq + hq] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+  walk<S::RT, kStreamKeys, D, kStreamThreads>(a, pre, [&](const Tile &tile, int lo, int hi, int slot) {
+    S::segment(a, L, tile, lo, hi, slot, gridDim.x);
+  });
 }
 
 }  // namespace k3

@@ -15,17 +15,26 @@ hipError_t launch_attn_bf16_e4m3(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_f16(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_f16_e4m3(const AttnArgs &a, hipStream_t s);
 
-int attn_workgroups() { return 2 * num_cus(); }
-
-// Rows per tile: the smallest that holds an average request's rows.
+// Rows per tile: the smallest that holds an average request's rows. Up to 64
+// (32 at a head of 256) the streaming kernel's, two workgroups to a CU; above,
+// the tiled kernel's, eight waves to a CU.
 int attn_tile_rows(int T, int G, int R, int D) {
   const long long rows = ((long long)T * G + R - 1) / R;
-  return rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : 64;
+  if (rows <= 16) return 16;
+  if (rows <= 32) return 32;
+  if (rows <= 64 && D < 256) return 64;
+  return rows <= 128 ? 128 : 256;
+}
+
+int attn_workgroups(int tile_rows) {
+  const int cus = std::min(num_cus(), kMaxWorkgroups / 2);
+  return tile_rows == 256 ? cus : 2 * cus;
 }
 
 size_t attn_workspace_bytes(int T, int Hq, int n_heads, int D) {
-  // R is not known here: the tile for one request is the largest
-  return part_bytes(attn_tile_rows(T, Hq / n_heads, 1, D), D, attn_workgroups());
+  // R is not known here, and more requests only make the tiles smaller
+  const int rows = attn_tile_rows(T, Hq / n_heads, 1, D);
+  return part_bytes(rows, D, attn_workgroups(rows));
 }
 
 hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t s) {
