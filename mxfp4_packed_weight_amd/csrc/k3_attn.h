@@ -31,6 +31,9 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
+// A block for a tile of up to half the waves' rows takes 10 / 16 of the time
+// of a full one.
+constexpr int kHalfCost = 10;
 constexpr int kMaxWorkgroups = 1024;  // of a launch: at most two to a CU
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The running maximum is raised only by more than this (in powers of two):
@@ -58,88 +61,98 @@ __device__ __forceinline__ Request request_of(const AttnArgs &a, int r) {
 }
 
 // The cost of a request's tiles, in sixteenths of a place: the first tile's,
-// and what each next one has more. T * Hq <= 2^30 rows and 2^30 places keep
-// all sums below 2^61.
-template <int RT, int KB>
+// what each next one has more, and the last one's, which counts for less if it
+// is of up to HALF rows. T * Hq <= 2^30 rows and 2^30 places keep all sums
+// below 2^61.
+template <int RT, int KB, int HALF>
 struct Cost {
-  int tiles;
-  long long base, slope;
+  int tiles, last_rows;
+  long long base, slope, all;
   static constexpr long long kFixed = 16 * KB;  // queries in, results out
   __device__ __forceinline__ Cost(const AttnArgs &a, const Request &q) {
-    tiles = (int)(((long long)q.n * a.G + RT - 1) / RT);
+    const long long rows = (long long)q.n * a.G;
+    tiles = (int)((rows + RT - 1) / RT);
+    last_rows = (int)(rows - (long long)(tiles - 1) * RT);
     const bool causal = !a.mask && q.len >= q.n;
     slope = causal ? 16 * RT / a.G : 0;
     base = kFixed + 16ll * (causal ? q.len - q.n : q.len) + slope;
+    all = tiles ? of_first(tiles - 1) + of(tiles - 1) : 0;
   }
-  // of the first x tiles of a key head, of tile x
+  // a tile's cost per 16 of `base`; the first x tiles of a key head; tile x
+  __device__ __forceinline__ int weight(int x) const { return x == tiles - 1 && last_rows <= HALF ? kHalfCost : 16; }
   __device__ __forceinline__ long long of_first(long long x) const { return x * base + slope * (x * (x - 1) / 2); }
-  __device__ __forceinline__ long long of(int x) const { return base + slope * x; }
-  __device__ __forceinline__ long long of_request(const AttnArgs &a) const { return of_first(tiles) * a.c.n_heads; }
+  __device__ __forceinline__ long long of(int x) const { return (base + slope * x) * weight(x) / 16; }
+  __device__ __forceinline__ long long of_request(const AttnArgs &a) const { return all * a.c.n_heads; }
 };
 
-// pre[r] = cost before request r, pre[R] = all of it; a workgroup of
-// THREADS threads. Ends with a barrier.
-template <int RT, int KB, int THREADS>
-__device__ __forceinline__ void line_of_tiles(const AttnArgs &a, long long *pre) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  __shared__ long long wave_sum[THREADS / 64];
-  if (a.R == 1) {
-    if (tid == 0) {
-      pre[0] = 0;
-      pre[1] = Cost<RT, KB>(a, request_of(a, 0)).of_request(a);
-    }
-    __syncthreads();
-    return;
-  }
-  const int per = (a.R + THREADS - 1) / THREADS;
-  const int lo = min(a.R, tid * per), hi = min(a.R, lo + per);
+// The requests go to the THREADS threads of a workgroup in runs of `per`.
+// pre[i] = cost before thread i's, pre[THREADS] = all of it. Ends with a
+// barrier.
+template <int THREADS>
+struct Line {
+  long long pre[THREADS + 1], wave_sum[THREADS / 64];
+};
+template <int THREADS>
+__device__ __forceinline__ int run_of(int R) { return (R + THREADS - 1) / THREADS; }
+
+template <int RT, int KB, int HALF, int THREADS>
+__device__ __forceinline__ void line_of_tiles(const AttnArgs &a, Line<THREADS> &L) {
+  const int tid = threadIdx.x, lane = tid & 63, per = run_of<THREADS>(a.R);
   long long own = 0;
-  for (int r = lo; r < hi; r++) {
-    pre[r] = own;
-    own += Cost<RT, KB>(a, request_of(a, r)).of_request(a);
-  }
+  for (int r = tid * per; r < min(a.R, tid * per + per); r++) own += Cost<RT, KB, HALF>(a, request_of(a, r)).of_request(a);
   long long incl = own;
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) {
     const long long x = __shfl_up(incl, m);
     if (lane >= m) incl += x;
   }
-  if (lane == 63) wave_sum[tid >> 6] = incl;
+  if (lane == 63) L.wave_sum[tid >> 6] = incl;
   __syncthreads();
   long long base = incl - own;
-  for (int w = 0; w < (tid >> 6); w++) base += wave_sum[w];
-  for (int r = lo; r < hi; r++) pre[r] += base;
-  if (hi == a.R && lo < hi) pre[a.R] = base + own;
+  for (int w = 0; w < (tid >> 6); w++) base += L.wave_sum[w];
+  L.pre[tid] = base;
+  if (tid == THREADS - 1) L.pre[THREADS] = base + own;
   __syncthreads();
 }
 
-// The request that place u of the line belongs to: the last r with pre[r] <= u.
-__device__ __forceinline__ int request_at(const long long *pre, int R, long long u) {
-  int lo = 0, hi = R - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= u) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
+// Values that are the same in all lanes, as such.
+__device__ __forceinline__ long long in_all_lanes(long long x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)x), hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
+  return (long long)((uint64_t)hi << 32 | lo);
 }
 
 // A tile in the line.
 struct Tile {
   Request q;
-  int r, h, row0;
+  int r, h, row0, rows;
   int places, blocks;      // that its rows may see: the first `places`, in `blocks` blocks
+  int weight;              // Cost::weight
   long long first, after;  // its stretch of the line
 };
-template <int RT, int KB>
-__device__ __forceinline__ Tile tile_at(const AttnArgs &a, const long long *pre, long long u) {
+template <int RT, int KB, int HALF, int THREADS>
+__device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &L, long long u) {
   Tile t;
-  t.r = request_at(pre, a.R, u);
+  // the last thread whose requests begin at or before it, and its request
+  const int per = run_of<THREADS>(a.R);
+  int run = 0, last = (a.R - 1) / per;
+  while (run < last) {
+    const int mid = (run + last + 1) >> 1;
+    if (in_all_lanes(L.pre[mid]) <= u) run = mid;
+    else last = mid - 1;
+  }
+  long long before = in_all_lanes(L.pre[run]);
+  t.r = run * per;
   t.q = request_of(a, t.r);
-  const Cost<RT, KB> cost(a, t.q);
-  const long long x = u - pre[t.r], head = cost.of_first(cost.tiles);
-  t.h = (int)(x / head);
-  const long long in_head = x - t.h * head;
+  for (; t.r + 1 < min(a.R, run * per + per); t.r++) {
+    const long long all = Cost<RT, KB, HALF>(a, t.q).of_request(a);
+    if (before + all > u) break;
+    before += all;
+    t.q = request_of(a, t.r + 1);
+  }
+  const Cost<RT, KB, HALF> cost(a, t.q);
+  const long long x = u - before;
+  t.h = (int)(x / cost.all);
+  const long long in_head = x - t.h * cost.all;
   int lo = 0, hi = cost.tiles - 1;  // the last tile that begins at or before it
   while (lo < hi) {
     const int mid = lo + ((hi - lo + 1) >> 1);
@@ -147,14 +160,12 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const long long *pre,
     else hi = mid - 1;
   }
   t.row0 = lo * RT;
-  t.first = pre[t.r] + t.h * head + cost.of_first(lo);
+  t.rows = lo == cost.tiles - 1 ? cost.last_rows : RT;
+  t.weight = cost.weight(lo);
+  t.first = before + t.h * cost.all + cost.of_first(lo);
   t.after = t.first + cost.of(lo);
   t.places = t.q.len;
-  if (!a.mask) {
-    const long long rows = (long long)t.q.n * a.G;
-    const int last = (int)((min(rows, (long long)t.row0 + RT) - 1) / a.G);
-    t.places = min(t.q.len, max(0, t.q.len - t.q.n + last + 1));
-  }
+  if (!a.mask) t.places = min(t.q.len, max(0, t.q.len - t.q.n + (t.row0 + t.rows - 1) / a.G + 1));
   t.blocks = t.places > 0 ? (t.places - 1) / KB + 1 : 1;
   return t;
 }
@@ -164,8 +175,9 @@ template <int KB>
 __device__ __forceinline__ int block_from(const Tile &t, long long u) {
   if (u <= t.first) return 0;
   if (u >= t.after) return t.blocks;
-  const long long y = max(u - t.first - Cost<16, KB>::kFixed, 0ll);
-  return (int)min((y + 16 * KB - 1) / (16 * KB), (long long)t.blocks);
+  const int each = KB * t.weight;  // a block's cost; as much is fixed
+  const long long y = max(u - t.first - each, 0ll);
+  return (int)min((y + each - 1) / each, (long long)t.blocks);
 }
 
 // Where workgroup b's stretch of the line begins.
@@ -181,15 +193,15 @@ __device__ __forceinline__ int place_in_line(int b, int B) { return B % 8 ? b : 
 
 // ---- partial results --------------------------------------------------------
 
-// part: for 2 B slots [RT][D] sums, then for each slot [RT] maxima, [RT] sums,
-// then B jobs of the joining launch.
-template <int RT, int D>
+// part: for 2 B slots [part_rows][D] sums, then for each slot [part_rows]
+// maxima, [part_rows] sums, then the jobs of the joining launch.
+template <int D>
 __device__ __forceinline__ float *part_o(const AttnArgs &a, int slot, int row) {
-  return a.part + ((size_t)slot * RT + row) * D;
+  return a.part + ((size_t)slot * a.part_rows + row) * D;
 }
-template <int RT, int D>
+template <int D>
 __device__ __forceinline__ float *part_ml(const AttnArgs &a, int B, int slot) {
-  return a.part + (size_t)2 * B * RT * D + (size_t)slot * 2 * RT;
+  return a.part + (size_t)2 * B * a.part_rows * D + (size_t)slot * 2 * a.part_rows;
 }
 // What workgroup b leaves to be joined: the tile that began in its stretch and
 // goes on up to workgroup `last`'s (rows = 0: none). Slots are -1 where it had
@@ -199,25 +211,23 @@ struct JoinJob {
   int tail_slot, head_slot;  // its own part of that tile; of a tile from before its stretch
   int pad;
 };
-template <int RT, int D>
+template <int D>
 __device__ __forceinline__ JoinJob *join_jobs(const AttnArgs &a, int B) {
-  return (JoinJob *)(a.part + (size_t)2 * B * RT * (D + 2));
-}
-inline size_t part_bytes(int RT, int D, int B) {
-  return (size_t)2 * B * RT * (D + 2) * sizeof(float) + kMaxWorkgroups * sizeof(JoinJob);
+  return (JoinJob *)(a.part + (size_t)2 * B * a.part_rows * (D + 2));
 }
 
 // The walk of a workgroup over its stretch of the line, with
 // segment(tile, first block, block after the last, slot or -1).
-template <int RT, int KB, int D, int THREADS, class Segment>
-__device__ __forceinline__ void walk(const AttnArgs &a, long long *pre, Segment &&segment) {
-  line_of_tiles<RT, KB, THREADS>(a, pre);
+template <int RT, int KB, int HALF, int D, int THREADS, class Segment>
+__device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
+  __shared__ Line<THREADS> L;
+  line_of_tiles<RT, KB, HALF, THREADS>(a, L);
   const int B = gridDim.x, b = place_in_line(blockIdx.x, B);
-  const Stretches line(pre[a.R], B);
+  const Stretches line(in_all_lanes(L.pre[THREADS]), B);
   const long long begin = line.begin(b), end = line.begin(b + 1);
   JoinJob job = {0, 0, 0, 0, -1, -1, -1, 0};
   for (long long u = begin; u < end;) {
-    const Tile tile = tile_at<RT, KB>(a, pre, u);
+    const Tile tile = tile_at<RT, KB, HALF>(a, L, u);
     const int lo = block_from<KB>(tile, u), hi = block_from<KB>(tile, end);
     const int slot = lo == hi || (lo == 0 && hi == tile.blocks) ? -1 : lo ? 2 * b : 2 * b + 1;
     if (u > tile.first) job.head_slot = slot;
@@ -225,7 +235,7 @@ __device__ __forceinline__ void walk(const AttnArgs &a, long long *pre, Segment 
       job.t0 = tile.q.t0;
       job.h = tile.h;
       job.row0 = tile.row0;
-      job.rows = min(RT, tile.q.n * a.G - tile.row0);
+      job.rows = tile.rows;
       job.tail_slot = slot;
       job.last = b;
       while (job.last + 1 < B && line.begin(job.last + 1) < tile.after) job.last++;
@@ -233,7 +243,7 @@ __device__ __forceinline__ void walk(const AttnArgs &a, long long *pre, Segment 
     if (lo < hi) segment(tile, lo, hi, slot);
     u = tile.after;
   }
-  if (threadIdx.x == 0) join_jobs<RT, D>(a, B)[b] = job;
+  if (threadIdx.x == 0) join_jobs<D>(a, B)[b] = job;
 }
 
 // ---- numbers ----------------------------------------------------------------

@@ -14,11 +14,11 @@ namespace k3 {
 
 constexpr int kJoinWaves = 4;
 
-template <bool BF, int D, int RT>
+template <bool BF, int D>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, int B) {
   __shared__ int lists[kJoinWaves][kMaxWorkgroups + 1];
   const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const JoinJob *jobs = join_jobs<RT, D>(a, B);
+  const JoinJob *jobs = join_jobs<D>(a, B);
   const JoinJob job = jobs[b];
   if ((int)blockIdx.y * kJoinWaves + wave >= job.rows) return;
   int *slots = lists[wave], n = 0;
@@ -44,10 +44,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
 #pragma unroll
       for (int i = 0; i < kAhead; i++) {
         const int x = x0 + i * SIDE + sub, slot = slots[min(x, n - 1)];
-        const float *ml = part_ml<RT, D>(a, B, slot);
+        const float *ml = part_ml<D>(a, B, slot);
         m[i] = ml[r];
-        s[i] = ml[RT + r];
-        p[i] = *(const f32x4 *)(part_o<RT, D>(a, slot, r) + d);
+        s[i] = ml[a.part_rows + r];
+        p[i] = *(const f32x4 *)(part_o<D>(a, slot, r) + d);
       }
 #pragma unroll
       for (int i = 0; i < kAhead; i++)

@@ -1,45 +1,41 @@
 // Which attention kernel a call takes, and its launches.
 #pragma once
 
+#include <algorithm>
+
 #include "k3_attn_join.h"
 #include "k3_attn_stream.h"
 #include "k3_attn_tile.h"
 
 namespace k3 {
 
-template <bool BF, int D, int RT>
+template <bool BF, int D>
 hipError_t launch_join(const AttnArgs &a, int B, hipStream_t s) {
   if (const hipError_t e = hipGetLastError()) return e;
-  attn_join_kernel<BF, D, RT><<<dim3(B, RT < 128 ? RT / kJoinWaves : RT / (2 * kJoinWaves)), 64 * kJoinWaves, 0, s>>>(a, B);
+  attn_join_kernel<BF, D><<<dim3(B, std::min((a.part_rows + kJoinWaves - 1) / kJoinWaves, 32)), 64 * kJoinWaves, 0, s>>>(a, B);
   return hipGetLastError();
 }
 
 template <bool BF, bool F8, int D, int QT>
 hipError_t launch_stream(const AttnArgs &a, hipStream_t s) {
   const int B = attn_workgroups(16 * QT);
-  const size_t pre = (a.R + 1) * sizeof(long long);
-  attn_stream_kernel<BF, F8, D, QT><<<B, kStreamThreads, pre, s>>>(a);
-  return launch_join<BF, D, 16 * QT>(a, B, s);
+  attn_stream_kernel<BF, F8, D, QT><<<B, kStreamThreads, 0, s>>>(a);
+  return launch_join<BF, D>(a, B, s);
 }
 
-template <bool BF, bool F8, int D, int NW>
+template <bool BF, bool F8, int D>
 hipError_t launch_tile(const AttnArgs &a, hipStream_t s) {
-  const int B = attn_workgroups(32 * NW);
-  const size_t pre = (a.R + 1) * sizeof(long long);
-  attn_tile_kernel<BF, F8, D, NW><<<B, 64 * NW, pre, s>>>(a);
-  return launch_join<BF, D, 32 * NW>(a, B, s);
+  const int B = attn_workgroups(kAttnRows);
+  attn_tile_kernel<BF, F8, D><<<B, kAttnThreads, 0, s>>>(a);
+  return launch_join<BF, D>(a, B, s);
 }
 
 template <bool BF, bool F8, int D>
 hipError_t launch_attn(const AttnArgs &a, hipStream_t s) {
-  switch (attn_tile_rows(a.T, a.G, a.R, D)) {
+  switch (attn_tile_rows(a.T, a.G, a.R)) {
     case 16: return launch_stream<BF, F8, D, 1>(a, s);
     case 32: return launch_stream<BF, F8, D, 2>(a, s);
-    case 64:
-      if constexpr (D < 256) return launch_stream<BF, F8, D, 4>(a, s);
-      return hipErrorInvalidValue;
-    case 128: return launch_tile<BF, F8, D, 4>(a, s);
-    default: return launch_tile<BF, F8, D, 8>(a, s);
+    default: return launch_tile<BF, F8, D>(a, s);
   }
 }
 

@@ -391,11 +391,11 @@ struct Stream {
           *(u32x2 *)(a.out + tok * a.out_stride + hq * D + d) = y;
           if (a.lse && d == 0) a.lse[tok * a.Hq + hq] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         } else {
-          *(f32x4 *)(part_o<RT, D>(a, slot, 16 * t + rr) + d) = o;
+          *(f32x4 *)(part_o<D>(a, slot, 16 * t + rr) + d) = o;
           if (d == 0) {
-            float *ml = part_ml<RT, D>(a, B, slot);
+            float *ml = part_ml<D>(a, B, slot);
             ml[16 * t + rr] = top;
-            ml[RT + 16 * t + rr] = sum;
+            ml[a.part_rows + 16 * t + rr] = sum;
           }
         }
       }
@@ -407,9 +407,8 @@ struct Stream {
 template <bool BF, bool F8, int D, int QT>
 __global__ __launch_bounds__(kStreamThreads) void attn_stream_kernel(AttnArgs a) {
   using S = Stream<BF, F8, D, QT>;
-  extern __shared__ long long pre[];
   __shared__ typename S::Lds L;
-  walk<S::RT, kStreamKeys, D, kStreamThreads>(a, pre, [&](const Tile &tile, int lo, int hi, int slot) {
+  walk<S::RT, kStreamKeys, 0, D, kStreamThreads>(a, [&](const Tile &tile, int lo, int hi, int slot) {
     S::segment(a, L, tile, lo, hi, slot, gridDim.x);
   });
 }

@@ -1,12 +1,14 @@
 // Attention for many rows per key head: prompts, and trees whose nodes times
 // the group's heads fill the matrix unit.
 //
-// The two products bound the time. A workgroup's NW waves have 32 rows each
-// and share blocks of KB keys and values in LDS, two blocks in turn: while
-// one is used the other arrives (16-bit caches go from memory to LDS without
-// registers; e4m3 ones are widened on the way, once per workgroup), and one
-// barrier per block changes them over. As in the streaming kernel all is
-// transposed (lane l, c = l % 32, h = l / 32):
+// The two products bound the time, and next to them the exponentials. Eight
+// waves of 32 rows share blocks of KB keys and values in LDS. Blocks are
+// fetched kAhead turns before their use, straight from memory to LDS (e4m3
+// ones into a ring of their own, and widened from there one turn ahead, once
+// for all waves), with one barrier per block. A tile of up to 128 rows would
+// leave half of the waves without work: there, two waves share 32 rows, each
+// has half of every block, and they join their results at the end.
+// As in the streaming kernel all is transposed (lane l, c = l % 32, h = l / 32):
 //   S^T = K Q^T   rows: 32 places, columns: the wave's 32 rows. The lane has
 //                 row c's scores of places 8 b + 4 h + 0..3.
 //   O^T = V^T P^T 16 places per product in the order in which the lane has
@@ -35,26 +37,34 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c) {
                                                 0);
 }
 
-// What places outside every page read.
-static __device__ const uint4 kZeroRow[256 * 2 / 16] = {};
-
+constexpr int kAttnWaves = 8, kAttnRows = 32 * kAttnWaves, kAttnThreads = 64 * kAttnWaves;
 template <int D>
-constexpr int kTileKeys = D == 256 ? 32 : 64;
+constexpr int kAttnKeys = D == 256 ? 32 : 64;
+// Tiles of so many rows go two waves to 32 rows (not with blocks of 32).
+template <int D>
+constexpr int kPairedRows = kAttnKeys<D> == 64 ? kAttnRows / 2 : 0;
 
-template <bool BF, bool F8, int D, int NW>
+template <bool BF, bool F8, int D>
 struct Tiled {
-  static constexpr int RT = 32 * NW, KB = kTileKeys<D>, KT = KB / 32;
+  static constexpr int NW = kAttnWaves, RT = kAttnRows, KB = kAttnKeys<D>;
   static constexpr int NS = D / 16, DT = D / 32;     // steps over the head, tiles of the output
-  static constexpr int ROW = 2 * D, CH = D / 8;      // a row of LDS, its chunks
-  static constexpr int RPI = 64 / CH;                // rows per load of a wave
-  static constexpr int RPW = KB / NW, NI = RPW / RPI;  // rows and loads of a wave
-  static constexpr int kBlock = KB * ROW, kBuffer = 2 * kBlock;
+  static constexpr int ROW = 2 * D;                  // a row of LDS, D / 8 chunks
   static constexpr int ES = F8 ? 1 : 2;
-  static_assert(NI * RPI == RPW && NI >= 1, "");
+  static constexpr int CH = D * ES / 16;             // chunks of a row of the cache
+  static constexpr int RPL = 64 / CH;                // rows per load of a wave
+  static constexpr int NL = 2 * KB / RPL / NW;       // loads of a wave, keys and values
+  static constexpr int kBlock = KB * ROW, kBuffer = 2 * kBlock, kRaw = 2 * KB * D;
+  static constexpr int kAhead = F8 ? 3 : 2;
+  static constexpr int kBuffers = F8 ? 2 : kAhead + 1, kRaws = F8 ? kAhead : 0;
+  static constexpr int kInFlight = (F8 ? kAhead - 2 : kAhead - 1) * NL;
+  static constexpr int kListed = 64;                 // blocks in the list of rows
+  static_assert(NL >= 1 && NL * NW * RPL == 2 * KB, "");
 
   struct Lds {
-    alignas(16) char buf[2][kBuffer];  // keys, then values
-    int odd;  // a block's values held ones that are not finite
+    alignas(16) char buf[kBuffers * kBuffer + kRaws * kRaw];  // blocks: keys, then values
+    int64_t row[kListed * KB];  // where the places' rows are, of 64 blocks in turn
+    uint64_t present[kListed];  // which places of a block are there
+    int odd;                    // a block's values held ones that are not finite
   };
 
   struct Wave {
@@ -62,15 +72,6 @@ struct Tiled {
     f32x16 o[DT];
     float ref, sum;  // the reference exponent, this lane's part of the sum
   };
-  struct Staged {  // e4m3 rows on their way
-    u32x2 k[F8 ? NI : 1], v[F8 ? NI : 1];
-  };
-  // A block's pages, one place per lane (blocks of 32: each place twice).
-  struct Places {
-    int64_t offset;
-    uint64_t present;
-  };
-
   static __device__ __forceinline__ int swizzle_k(int row) {
     return D == 64 ? (row & 7) ^ ((row >> 3) & 1) : row & 15;
   }
@@ -79,77 +80,92 @@ struct Tiled {
     return D == 64 ? 2 * r : 2 * (2 * r ^ (r >> 1));
   }
 
-  static __device__ __forceinline__ int table_entry(const AttnArgs &a, const int32_t *row, int p, int len) {
-    if (p >= len) return -1;
+  // Byte offset of a place's row; -1 if it has no page.
+  static __device__ __forceinline__ int64_t place(const AttnArgs &a, const int32_t *table, int p, int end) {
+    if (p >= end) return -1;
     const uint32_t b = __umulhi(2u * (uint32_t)p, a.page_magic) >> a.page_shift;
-    return b < (uint32_t)a.blocks ? row[b] : -1;
+    const int page = b < (uint32_t)a.blocks ? table[b] : -1;
+    if (page < 0 || page >= a.c.n_pages) return -1;
+    return (page * a.c.page_stride + (int)((uint32_t)p - b * a.c.page_size) * a.c.slot_stride) * ES;
   }
-  static __device__ __forceinline__ Places places(const AttnArgs &a, int p, int page) {
-    const bool there = page >= 0 && page < a.c.n_pages;
-    const uint32_t b = __umulhi(2u * (uint32_t)p, a.page_magic) >> a.page_shift;
-    const int64_t at = page * a.c.page_stride + (int)((uint32_t)p - b * a.c.page_size) * a.c.slot_stride;
-    return {there ? at * ES : 0, __ballot(there)};
+  // Lists half of the 64 blocks, from block x on, and says which of them have
+  // places that are not there (their rows are read from the cache's first).
+  static __device__ __forceinline__ uint64_t list(const AttnArgs &a, Lds &L, const int32_t *table, int x, int end,
+                                                  uint64_t holes) {
+    const int at = x % kListed;
+#pragma unroll
+    for (int i = 0; i < kListed / 2 * KB / kAttnThreads; i++) {
+      const int n = i * kAttnThreads + threadIdx.x;
+      const int64_t row = place(a, table, x * KB + n, end);
+      L.row[at * KB + n] = row < 0 ? 0 : row;
+      const uint64_t there = __ballot(row >= 0);
+      const int lane = n & 63;
+      if (KB == 64 && lane == 0) L.present[at + n / KB] = there;
+      if (KB == 32 && lane % 32 == 0) L.present[at + n / KB] = there >> lane | 0xffffffff00000000ull;
+    }
+    __syncthreads();
+    const uint64_t mine = __ballot(L.present[at + threadIdx.x % (kListed / 2)] != ~0ull) & 0xffffffffu;
+    return (holes & ~(0xffffffffull << at)) | mine << at;
   }
 
-  // This wave's rows of a block: into LDS, or (e4m3) into registers.
-  static __device__ __forceinline__ void fetch(const Places &pl, const char *k, const char *v, lds_char *buf, Staged &st,
-                                               int lane, int wave) {
-    const int pos = lane % CH;
-    const bool full = pl.present == ~0ull;
+  // A copy of 16 bytes per lane from memory to LDS, in order from `to` on. The
+  // compiler is not to know: it would have every read of LDS wait for it.
+  // change_over() is what waits.
+  static __device__ __forceinline__ void copy(const char *from, lds_char *to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to)), "v"(from)
+                 : "memory");
+  }
+  // This wave's loads of block x.
+  static __device__ __forceinline__ void fetch(const Lds &L, int x, const char *k, const char *v, lds_char *to,
+                                               uint32_t lane, int wave) {
+    const uint32_t pos = lane % CH, sub = lane / CH;
+    const int64_t *rows = L.row + x % kListed * KB + sub;
 #pragma unroll
-    for (int i = 0; i < NI; i++) {
-      const int row = wave * RPW + i * RPI + lane / CH;
-      const uint32_t lo = __shfl((int)(uint32_t)pl.offset, row), hi = __shfl((int)(pl.offset >> 32), row);
-      const int64_t at = (int64_t)((uint64_t)hi << 32 | lo);
-      if constexpr (F8) {
-        const bool there = (pl.present >> row) & 1;
-        st.k[i] = *(const u32x2 *)(k + at + 8 * pos);
-        st.v[i] = *(const u32x2 *)(v + at + 8 * pos);
-        if (!there) st.k[i] = st.v[i] = u32x2{0, 0};
-      } else {
-        const int kc = 16 * (pos ^ swizzle_k(row)), vc = 16 * (pos ^ swizzle_v(row));
-        const char *kp = k + at + kc, *vp = v + at + vc;
-        if (!full && !((pl.present >> row) & 1)) {
-          kp = (const char *)kZeroRow + kc;
-          vp = (const char *)kZeroRow + vc;
-        }
-        lds_char *to = buf + (wave * RPW + i * RPI) * ROW;
-        __builtin_amdgcn_global_load_lds((global_ptr)kp, (__attribute__((address_space(3))) void *)to, 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((global_ptr)vp, (__attribute__((address_space(3))) void *)(to + kBlock), 16, 0,
-                                         0);
-      }
+    for (int i = 0; i < NL; i++) {
+      const bool values = NL > 1 ? i & 1 : wave >= NW / 2;
+      const int group = NL > 1 ? wave * (NL / 2) + i / 2 : wave % (NW / 2), first = group * RPL;
+      // (the swizzles are linear in the bits of the row)
+      const int chunk = F8 ? 16 * pos
+                           : values ? 16 * (pos ^ swizzle_v(sub)) ^ 16 * swizzle_v(first)
+                                    : 16 * (pos ^ swizzle_k(sub)) ^ 16 * swizzle_k(first);
+      copy((values ? v : k) + rows[first] + chunk, to + (values ? KB * CH * 16 : 0) + group * 1024);
     }
   }
-  static __device__ __forceinline__ void put(const Staged &st, lds_char *buf, int lane, int wave) {
-    if constexpr (F8) {
-      const int pos = lane % CH;
-      auto wide = [](u32x2 w) {
-        return u32x4{widen2<BF, false>(w[0]), widen2<BF, true>(w[0]), widen2<BF, false>(w[1]), widen2<BF, true>(w[1])};
-      };
+  // A block of e4m3 rows from LDS into LDS.
+  static __device__ __forceinline__ void widen(const lds_char *from, lds_char *to) {
+    auto wide = [](uint32_t x, uint32_t y) {
+      return u32x4{widen2<BF, false>(x), widen2<BF, true>(x), widen2<BF, false>(y), widen2<BF, true>(y)};
+    };
 #pragma unroll
-      for (int i = 0; i < NI; i++) {
-        const int row = wave * RPW + i * RPI + lane / CH;
-        lds_char *to = buf + row * ROW;
-        *(__attribute__((address_space(3))) u32x4 *)(to + 16 * (pos ^ swizzle_k(row))) = wide(st.k[i]);
-        *(__attribute__((address_space(3))) u32x4 *)(to + kBlock + 16 * (pos ^ swizzle_v(row))) = wide(st.v[i]);
-      }
+    for (int i = 0; i < kRaw / 16 / kAttnThreads; i++) {
+      const int x = i * kAttnThreads + threadIdx.x;  // a chunk: two of the wide row
+      const int row = x / CH, chunk = 2 * (x % CH);
+      const u32x4 w = *(const __attribute__((address_space(3))) u32x4 *)(from + 16 * x);
+      const int f = row < KB ? swizzle_k(row) : swizzle_v(row);
+      *(__attribute__((address_space(3))) u32x4 *)(to + row * ROW + 16 * (chunk ^ f)) = wide(w[0], w[1]);
+      *(__attribute__((address_space(3))) u32x4 *)(to + row * ROW + 16 * ((chunk + 1) ^ f)) = wide(w[2], w[3]);
     }
   }
 
-  // All of this wave's copies are in and its reads are done; then all waves'.
+  // All but the newest IN_FLIGHT of this wave's copies are in and its LDS
+  // accesses are done; then all waves'.
+  template <int IN_FLIGHT>
   static __device__ __forceinline__ void change_over() {
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(IN_FLIGHT) : "memory");
   }
 
-  // Values that are not finite numbers set to zero (0 times NaN would reach
-  // rows that do not see their place).
-  static __device__ __forceinline__ void make_finite(lds_char *v, int *odd) {
+  // Values at places that are not there, and those that are not finite
+  // numbers, set to zero (0 times NaN would reach rows that do not see them).
+  static __device__ __forceinline__ void make_finite(lds_char *v, uint64_t present, int *odd) {
     bool lost = false;
-    for (int x = threadIdx.x; x < kBlock / 16; x += 64 * NW) {
+    for (uint32_t x = threadIdx.x; x < kBlock / 16; x += kAttnThreads) {
       auto *p = (__attribute__((address_space(3))) u32x4 *)(v + 16 * x);
+      if (!((present >> (x / (ROW / 16))) & 1)) {
+        *p = u32x4{0, 0, 0, 0};
+        continue;
+      }
       u32x4 w = *p;
       uint32_t m = 0;
 #pragma unroll
@@ -166,11 +182,13 @@ struct Tiled {
     if (lost) *odd = 1;
   }
 
-  // The products of those values with the weights of the rows that see them.
+  // The products of those values with the weights of the rows that see them;
+  // KT tiles of 32 places from k0 on.
+  template <int KT>
   static __device__ __forceinline__ void add_not_finite(const AttnArgs &a, f32x16 *o, const float (*x)[16],
                                                         const uint32_t *vis, const char *v, const int32_t *table,
-                                                        int k0, uint64_t present, int len, int c, int h) {
-    for (int key = 0; key < KB; key++) {
+                                                        int k0, uint64_t present, int c, int h) {
+    for (int key = 0; key < 32 * KT; key++) {
       if (!((present >> key) & 1)) continue;
       const int at = (key >> 5) * 16 + ((key >> 3) & 3) * 4 + (key & 3);
       float mine = 0.f;
@@ -181,9 +199,7 @@ struct Tiled {
       uint32_t word = vis[0];
       if (KT > 1 && key >= 32) word = vis[KT - 1];
       const bool sees = (word >> (key & 31)) & 1;
-      const int page = table_entry(a, table, k0 + key, len);
-      const Places pl = places(a, k0 + key, page);
-      const char *row = v + pl.offset;
+      const char *row = v + place(a, table, k0 + key, INT32_MAX);
 #pragma unroll
       for (int t = 0; t < DT; t++)
 #pragma unroll
@@ -201,12 +217,13 @@ struct Tiled {
     }
   }
 
-  // One block of KB places for this wave's rows. PARTIAL: with places that
-  // some rows do not see; from: the first such place.
-  template <bool PARTIAL>
+  // KT tiles of 32 places, from k0 on, for this wave's rows; keys: their rows
+  // in LDS. PARTIAL: with places that some rows do not see; from: the first
+  // such place.
+  template <bool PARTIAL, int KT>
   static __device__ __forceinline__ void block(const AttnArgs &a, Wave &w, const Request &rq, int node, int k0,
-                                               int from, uint64_t present, float scale, lds_char *buf, bool odd,
-                                               const char *v, const int32_t *table, int lane) {
+                                               int from, uint64_t present, float scale, lds_char *keys, bool odd,
+                                               const char *v, const int32_t *table, uint32_t lane) {
     typedef const __attribute__((address_space(3))) u32x4 *row_ptr;
     typedef __attribute__((address_space(3))) s16x4 *tr_ptr;
     if (PARTIAL) asm volatile("" : "+v"(lane));  // nothing of this is kept in registers outside
@@ -214,19 +231,19 @@ struct Tiled {
     f32x16 s[KT];
     {
       const int f = h ^ swizzle_k(c);  // (the same for row c + 32)
-      const lds_char *row = buf + c * ROW;
+      const lds_char *row = keys + c * ROW;
 #pragma unroll
       for (int u = 0; u < KT; u++) s[u] = f32x16{};
       auto key = [&](int x) { return *(row_ptr)(row + 16 * (2 * (x / KT) ^ f) + 32 * (x % KT) * ROW); };
-      constexpr int N = NS * KT, kAhead = 4;
-      u32x4 k[kAhead];
+      constexpr int N = NS * KT, kReads = 4;
+      u32x4 k[kReads];
 #pragma unroll
-      for (int x = 0; x < kAhead; x++) k[x] = key(x);
+      for (int x = 0; x < kReads; x++) k[x] = key(x);
 #pragma unroll
       for (int x = 0; x < N; x++) {
-        __builtin_amdgcn_sched_barrier(0);  // reads stay kAhead products ahead
-        s[x % KT] = mfma32<BF>(k[x % kAhead], w.q[x / KT], s[x % KT]);
-        if (x + kAhead < N) k[x % kAhead] = key(x + kAhead);
+        __builtin_amdgcn_sched_barrier(0);  // reads stay kReads products ahead
+        s[x % KT] = mfma32<BF>(k[x % kReads], w.q[x / KT], s[x % KT]);
+        if (x + kReads < N) k[x % kReads] = key(x + kReads);
       }
     }
     float x[KT][16];
@@ -237,7 +254,7 @@ struct Tiled {
       for (int i = 0; i < 16; i++) x[u][i] = s[u][i];
       if (PARTIAL) {
         vis[u] = (uint32_t)(present >> (32 * u));
-        if (k0 + KB > from) vis[u] = seen(a, rq, node, k0 + 32 * u, vis[u]);
+        if (k0 + 32 * KT > from) vis[u] = seen(a, rq, node, k0 + 32 * u, vis[u]);
 #pragma unroll
         for (int i = 0; i < 16; i++)
           if (!((vis[u] >> (8 * (i / 4) + 4 * h + i % 4)) & 1)) x[u][i] = -INFINITY;
@@ -262,7 +279,7 @@ struct Tiled {
     // lane i of a group of 16 reads row i / 4's values 4 (i % 4) + 0..3 of the
     // group's 4 x 16 and receives column i's
     const int i16 = lane & 15, key = 4 * h + i16 / 4, f = swizzle_v(key);
-    const lds_char *row = buf + kBlock + key * ROW + 8 * (i16 & 1);
+    const lds_char *row = keys + kBlock + key * ROW + 8 * (i16 & 1);
     auto value = [&](int j, int t) {  // places 16 j + 0..15, tile t of the head
       const lds_char *at = row + 16 * ((4 * t + 2 * ((lane >> 4) & 1) + ((i16 >> 1) & 1)) ^ f) + 16 * j * ROW;
       const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)at));
@@ -299,39 +316,29 @@ struct Tiled {
       }
     __builtin_amdgcn_sched_barrier(0);
     w.sum += part[0] + part[1];
-    if (PARTIAL && odd) add_not_finite(a, w.o, x, vis, v, table, k0, present, rq.len, c, h);
-  }
-
-  // A block is used while the next one arrives. The two buffers do not
-  // overlap: reads of `cur` need not wait for the copies into `next`.
-  template <bool PARTIAL>
-  static __device__ __forceinline__ void step(const AttnArgs &a, Wave &w, const Request &rq, int node, int k0,
-                                              int from, uint64_t present, const Places &then, bool more, bool use,
-                                              float scale, lds_char *__restrict__ cur, lds_char *__restrict__ next,
-                                              bool odd, const char *k, const char *v, const int32_t *table, int lane,
-                                              int wave) {
-    Staged st;
-    if (more) fetch(then, k, v, next, st, lane, wave);
-    if (use) block<PARTIAL>(a, w, rq, node, k0, from, present, scale, cur, odd, v, table, lane);
-    if (F8 && more) put(st, next, lane, wave);
+    if (PARTIAL && odd) add_not_finite<KT>(a, w.o, x, vis, v, table, k0, present, c, h);
   }
 
   // A tile's blocks [lo, hi): its result, or a partial one into `slot`.
+  // PAIRED: two waves for 32 rows, half of each block to each.
+  template <bool PAIRED>
   static __device__ __forceinline__ void segment(const AttnArgs &a, Lds &L, const Tile &tile, int lo, int hi, int slot,
                                                  int B) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31,
-              h = lane >> 5;
+    const uint32_t lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Request &rq = tile.q;
-    const int rows = rq.n * a.G, first_row = tile.row0 + 32 * wave, row = first_row + c;
+    const int first_in_tile = 32 * (PAIRED ? wave >> 1 : wave), in_tile = first_in_tile + (int)c;
+    const int rows = rq.n * a.G, first_row = tile.row0 + first_in_tile, row = tile.row0 + in_tile;
     const bool on = row < rows, any = first_row < rows;
     const int node = on ? row / a.G : 0, hq = tile.h * a.G + (on ? row - node * a.G : 0);
     Wave w;
     // a negative scale turns the queries round, so that the largest product
     // has the largest score
-    const uint32_t turn = a.scale < 0.f ? 0x80008000u : 0u;
+    const uint32_t round = a.scale < 0.f ? 0x80008000u : 0u;
     const uint16_t *q = a.q + (int64_t)(rq.t0 + node) * a.q_stride + hq * D + 8 * h;
 #pragma unroll
-    for (int s = 0; s < NS; s++) w.q[s] = on && a.scale != 0.f ? *(const u32x4 *)(q + 16 * s) ^ turn : u32x4{0, 0, 0, 0};
+    for (int s = 0; s < NS; s++)
+      w.q[s] = on && a.scale != 0.f ? *(const u32x4 *)(q + 16 * s) ^ round : u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int t = 0; t < DT; t++) w.o[t] = f32x16{};
     w.ref = -INFINITY;
@@ -346,59 +353,85 @@ struct Tiled {
     const int tile_from = a.mask ? ctx : ctx + tile.row0 / a.G + 1;
     const int from = a.mask || !any ? ctx : ctx + first_row / a.G + 1;
     const int until = !any ? 0 : a.mask ? rq.len : ctx + (min(first_row + 31, rows - 1)) / a.G + 1;
-    lds_char *cur = (lds_char *)L.buf[0], *next = (lds_char *)L.buf[1];
-    const int in_block = lane % KB;
-    int page = table_entry(a, table, lo * KB + in_block, rq.len);
-    Places now = places(a, lo * KB + in_block, page), then = now;
-    page = table_entry(a, table, (lo + 1) * KB + in_block, rq.len);
-    {
-      Staged st;
-      fetch(now, k, v, cur, st, lane, wave);
-      put(st, cur, lane, wave);
-    }
-    // blocks below `whole` are seen by all rows, but for pages that are not there
-    const int whole = min(hi, max(tile_from, 0) / KB);
-    for (int j = lo; j < hi;) {
-      for (; j < whole && now.present == ~0ull; j++) {
-        change_over();
-        const bool more = j + 1 < hi;
-        if (more) {
-          then = places(a, (j + 1) * KB + in_block, page);
-          page = table_entry(a, table, (j + 2) * KB + in_block, rq.len);
-        }
-        step<false>(a, w, rq, node, j * KB, from, ~0ull, then, more, any, scale, cur, next, false, k, v, table, lane,
-                    wave);
-        now = then;
-        lds_char *t = cur;
-        cur = next;
-        next = t;
+    const int end = min(hi * KB, rq.len);
+    constexpr int KT = PAIRED ? 1 : KB / 32;
+    const int half = PAIRED ? 32 * (wave & 1) : 0;
+    lds_char *buf = (lds_char *)L.buf, *ring = buf + kBuffers * kBuffer;
+    int cur = 0, raw = 0;  // the block in use, the ring's place that is fetched into
+    uint64_t holes = 0;    // blocks of the list with places that are not there
+    // Fetches block x and returns where the block to use is.
+    auto advance = [&](int x) {
+      lds_char *now = buf + cur * kBuffer;
+      if constexpr (F8) {
+        fetch(L, x, k, v, ring + raw * kRaw, lane, wave);
+        raw = raw + 1 == kRaws ? 0 : raw + 1;
+        widen(ring + raw * kRaw, buf + (1 - cur) * kBuffer);  // the oldest in the ring: the next to use
+        cur = 1 - cur;
+      } else {
+        fetch(L, x, k, v, buf + (cur == 0 ? kBuffers - 1 : cur - 1) * kBuffer, lane, wave);
+        cur = cur + 1 == kBuffers ? 0 : cur + 1;
       }
-      if (j >= hi) break;
+      return now;
+    };
+    holes = list(a, L, table, lo & -(kListed / 2), end, holes);
+    for (int j = lo - kAhead; j < hi; j++) {
+      // blocks that all rows see whole
+      if (j >= lo) {
+        const int next = (j + kAhead + kListed / 2 - 1) & -(kListed / 2);  // block to list from
+        const int whole = min(min(hi, max(tile_from, 0) / KB), next - kAhead);
+        for (; j < whole && !((holes >> (j % kListed)) & 1); j++) {
+          change_over<kInFlight>();
+          lds_char *now = advance(j + kAhead);
+          if (any)
+            block<false, KT>(a, w, rq, node, 0, 0, ~0ull, scale, now + half * ROW, false, v, table, lane);
+        }
+        if (j >= hi) break;
+      }
       const int k0 = j * KB;
-      change_over();
+      change_over<kInFlight>();
+      if ((j + kAhead) % (kListed / 2) == 0 && j + kAhead > lo)
+        holes = list(a, L, table, j + kAhead, end, holes);
+      lds_char *now = advance(j + kAhead);
+      if (j < lo) continue;
+      const uint64_t present = in_all_lanes(L.present[j % kListed]);
       bool odd = false;
-      if (k0 + KB > tile_from) {
+      if (k0 + KB > tile_from || present != ~0ull) {
         if (threadIdx.x == 0) L.odd = 0;
-        change_over();
-        make_finite(cur + kBlock, &L.odd);
-        change_over();
+        change_over<63>();
+        make_finite(now + kBlock, present, &L.odd);
+        change_over<63>();
         odd = L.odd != 0;
       }
-      const bool more = j + 1 < hi;
-      if (more) {
-        then = places(a, k0 + KB + in_block, page);
-        page = table_entry(a, table, k0 + 2 * KB + in_block, rq.len);
-      }
-      step<true>(a, w, rq, node, k0, from, now.present, then, more, k0 < until, scale, cur, next, odd, k, v, table,
-                 lane, wave);
-      now = then;
-      lds_char *t = cur;
-      cur = next;
-      next = t;
-      j++;
+      if (k0 + half < until)
+        block<true, KT>(a, w, rq, node, k0 + half, from, present >> half, scale, now + half * ROW, odd, v, table,
+                        lane);
     }
-    change_over();  // LDS is free for the next tile
-    const float sum = sum_xor32(w.sum);
+    change_over<0>();  // LDS is free
+    float sum = sum_xor32(w.sum);
+    if constexpr (PAIRED) {
+      float *theirs = (float *)L.buf + (wave >> 1) * (16 * DT + 2) * 64 + (int)lane;
+      if (wave & 1) {
+#pragma unroll
+        for (int t = 0; t < DT; t++)
+#pragma unroll
+          for (int i = 0; i < 16; i++) theirs[64 * (16 * t + i)] = w.o[t][i];
+        theirs[64 * 16 * DT] = w.ref;
+        theirs[64 * (16 * DT + 1)] = sum;
+      }
+      __syncthreads();
+      if (!(wave & 1)) {
+        const float m = theirs[64 * 16 * DT], top = fmaxf(w.ref, m);
+        const float mine = w.ref == top ? 1.f : exp2_hw(w.ref - top), other = m == top ? 1.f : exp2_hw(m - top);
+        sum = sum * mine + theirs[64 * (16 * DT + 1)] * other;
+        w.ref = top;
+#pragma unroll
+        for (int t = 0; t < DT; t++)
+#pragma unroll
+          for (int i = 0; i < 16; i++) w.o[t][i] = w.o[t][i] * mine + theirs[64 * (16 * t + i)] * other;
+      }
+      __syncthreads();
+      if (wave & 1) return;
+    }
     if (!on) return;
     if (slot < 0) {
       const float f = sum == 0.f ? 0.f : (a.c.v_scale ? a.c.v_scale[tile.h] : 1.f) / sum;
@@ -412,7 +445,7 @@ struct Tiled {
                                                    pack2<BF>(w.o[t][4 * b + 2] * f, w.o[t][4 * b + 3] * f)};
       if (a.lse && h == 0) a.lse[tok * a.Hq + hq] = sum == 0.f ? -INFINITY : (w.ref + log2f(sum)) * kLn2;
     } else {
-      float *out = part_o<RT, D>(a, slot, 32 * wave + c) + 4 * h;
+      float *out = part_o<D>(a, slot, in_tile) + 4 * h;
 #pragma unroll
       for (int t = 0; t < DT; t++)
 #pragma unroll
@@ -420,21 +453,21 @@ struct Tiled {
           *(f32x4 *)(out + 32 * t + 8 * b) =
               f32x4{w.o[t][4 * b], w.o[t][4 * b + 1], w.o[t][4 * b + 2], w.o[t][4 * b + 3]};
       if (h == 0) {
-        float *ml = part_ml<RT, D>(a, B, slot);
-        ml[32 * wave + c] = w.ref;
-        ml[RT + 32 * wave + c] = sum;
+        float *ml = part_ml<D>(a, B, slot);
+        ml[in_tile] = w.ref;
+        ml[a.part_rows + in_tile] = sum;
       }
     }
   }
 };
 
-template <bool BF, bool F8, int D, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a) {
-  using S = Tiled<BF, F8, D, NW>;
-  extern __shared__ long long pre[];
+template <bool BF, bool F8, int D>
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnArgs a) {
+  using S = Tiled<BF, F8, D>;
   __shared__ typename S::Lds L;
-  walk<S::RT, S::KB, D, 64 * NW>(a, pre, [&](const Tile &tile, int lo, int hi, int slot) {
-    S::segment(a, L, tile, lo, hi, slot, gridDim.x);
+  walk<S::RT, S::KB, kPairedRows<D>, D, kAttnThreads>(a, [&](const Tile &tile, int lo, int hi, int slot) {
+    if (kPairedRows<D> && tile.rows <= kPairedRows<D>) S::template segment<true>(a, L, tile, lo, hi, slot, gridDim.x);
+    else S::template segment<false>(a, L, tile, lo, hi, slot, gridDim.x);
   });
 }
 

@@ -40,13 +40,13 @@ struct AttnArgs {
   k3_kv_cache c;
   const int32_t *table, *cu, *kv_lens, *mask;
   uint16_t *out;
-  float *lse, *part;  // part: the partial results of split tiles
+  float *lse, *part;  // part: the partial results of split tiles, of up to part_rows rows
   float scale;
-  int dtype, T, Hq, G, blocks, R, words;
+  int dtype, T, Hq, G, blocks, R, words, part_rows;
   uint32_t page_magic;  // a place p < 2^31 is in block umulhi(2p, page_magic) >> page_shift
   int page_shift;
 };
-int attn_tile_rows(int T, int G, int R, int D);
+int attn_tile_rows(int T, int G, int R);
 int attn_workgroups(int tile_rows);
 size_t attn_workspace_bytes(int T, int Hq, int n_heads, int D);
 hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t s);

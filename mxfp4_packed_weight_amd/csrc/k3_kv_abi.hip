@@ -15,15 +15,11 @@ hipError_t launch_attn_bf16_e4m3(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_f16(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_f16_e4m3(const AttnArgs &a, hipStream_t s);
 
-// Rows per tile: the smallest that holds an average request's rows. Up to 64
-// (32 at a head of 256) the streaming kernel's, two workgroups to a CU; above,
-// the tiled kernel's, eight waves to a CU.
-int attn_tile_rows(int T, int G, int R, int D) {
+// Rows per tile: up to 32 rows of an average request go to the streaming
+// kernel, two workgroups to a CU; more to the tiled kernel, one to a CU.
+int attn_tile_rows(int T, int G, int R) {
   const long long rows = ((long long)T * G + R - 1) / R;
-  if (rows <= 16) return 16;
-  if (rows <= 32) return 32;
-  if (rows <= 64 && D < 256) return 64;
-  return rows <= 128 ? 128 : 256;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 256;
 }
 
 int attn_workgroups(int tile_rows) {
@@ -31,10 +27,13 @@ int attn_workgroups(int tile_rows) {
   return tile_rows == 256 ? cus : 2 * cus;
 }
 
+static int attn_part_rows(int tile_rows, int T, int G) { return (int)std::min((long long)tile_rows, (long long)T * G); }
+
 size_t attn_workspace_bytes(int T, int Hq, int n_heads, int D) {
   // R is not known here, and more requests only make the tiles smaller
-  const int rows = attn_tile_rows(T, Hq / n_heads, 1, D);
-  return part_bytes(rows, D, attn_workgroups(rows));
+  const int G = Hq / n_heads, rows = attn_tile_rows(T, G, 1);
+  return (size_t)2 * attn_workgroups(rows) * attn_part_rows(rows, T, G) * (D + 2) * sizeof(float) +
+         kMaxWorkgroups * sizeof(JoinJob);
 }
 
 hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t s) {
@@ -301,6 +300,7 @@ k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T, i
   a.blocks = blocks;
   a.R = R;
   a.words = words;
+  a.part_rows = attn_part_rows(attn_tile_rows(T, a.G, R), T, a.G);
   // p / P = (p * m) >> (31 + s) for p < 2^31: s = ceil(log2 P), m the next
   // integer above 2^(31 + s) / P (m < 2^32, and m P - 2^(31 + s) <= 2^s)
   int shift = 0;
