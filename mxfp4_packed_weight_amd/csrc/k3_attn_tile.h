@@ -2,12 +2,17 @@
 // the group's heads fill the matrix unit.
 //
 // The two products bound the time, and next to them the exponentials. Eight
-// waves of 32 rows share blocks of KB keys and values in LDS. Blocks are
+// waves of 32 rows share blocks of KB keys and values in LDS. A wave's turn
+// has two phases, one of products (the weights of the last block with its
+// values, then this block's keys with the queries) and one of arithmetic (the
+// scores' maximum, exponentials and sum). The two waves of a SIMD are a phase
+// apart, so that the matrix unit has the one's products while the vector unit
+// has the other's exponentials; a barrier per phase keeps them so. Blocks are
 // fetched kAhead turns before their use, straight from memory to LDS (e4m3
 // ones into a ring of their own, and widened from there one turn ahead, once
-// for all waves), with one barrier per block. A tile of up to 128 rows would
-// leave half of the waves without work: there, two waves share 32 rows, each
-// has half of every block, and they join their results at the end.
+// for all waves). A tile of up to 128 rows would leave half of the waves
+// without work: there, two waves share 32 rows, each has half of every block,
+// and they join their results at the end.
 // As in the streaming kernel all is transposed (lane l, c = l % 32, h = l / 32):
 //   S^T = K Q^T   rows: 32 places, columns: the wave's 32 rows. The lane has
 //                 row c's scores of places 8 b + 4 h + 0..3.
@@ -18,6 +23,8 @@
 // row's number, so that the reads of 32 rows' same chunk (keys) and of four
 // rows' neighbouring chunks (values) spread over the banks.
 #pragma once
+
+#include <type_traits>
 
 #include "k3_attn.h"
 
@@ -42,7 +49,7 @@ template <int D>
 constexpr int kAttnKeys = D == 256 ? 32 : 64;
 // Tiles of so many rows go two waves to 32 rows (not with blocks of 32).
 template <int D>
-constexpr int kPairedRows = kAttnKeys<D> == 64 ? kAttnRows / 2 : 0;
+constexpr int kPairedRows = kAttnKeys<D> >= 64 ? kAttnRows / 2 : 0;
 
 template <bool BF, bool F8, int D>
 struct Tiled {
@@ -57,18 +64,21 @@ struct Tiled {
   static constexpr int kAhead = F8 ? 3 : 2;
   static constexpr int kBuffers = F8 ? 2 : kAhead + 1, kRaws = F8 ? kAhead : 0;
   static constexpr int kInFlight = (F8 ? kAhead - 2 : kAhead - 1) * NL;
-  static constexpr int kListed = 64;                 // blocks in the list of rows
+  static constexpr int kListed = KB == 128 ? 32 : 64;  // blocks in the list of rows
   static_assert(NL >= 1 && NL * NW * RPL == 2 * KB, "");
 
   struct Lds {
-    alignas(16) char buf[kBuffers * kBuffer + kRaws * kRaw];  // blocks: keys, then values
-    int64_t row[kListed * KB];  // where the places' rows are, of 64 blocks in turn
-    uint64_t present[kListed];  // which places of a block are there
-    int odd;                    // a block's values held ones that are not finite
+    alignas(16) char buf[kBuffers * kBuffer + kRaws * kRaw];  // keys of a block, values of the one before
+    int64_t row[kListed * KB];  // where the places' rows are, of kListed blocks in turn
+    uint32_t present[kListed * KB / 32];  // which places of a block are there
+    int odd;                    // values that are not finite were set to zero
   };
 
+  template <int KT>
   struct Wave {
     u32x4 q[NS];
+    f32x16 s[KT];     // the block's scores
+    u32x4 p[2 * KT];  // its weights
     f32x16 o[DT];
     float ref, sum;  // the reference exponent, this lane's part of the sum
   };
@@ -88,7 +98,7 @@ struct Tiled {
     if (page < 0 || page >= a.c.n_pages) return -1;
     return (page * a.c.page_stride + (int)((uint32_t)p - b * a.c.page_size) * a.c.slot_stride) * ES;
   }
-  // Lists half of the 64 blocks, from block x on, and says which of them have
+  // Lists half of kListed blocks, from block x on, and says which of them have
   // places that are not there (their rows are read from the cache's first).
   static __device__ __forceinline__ uint64_t list(const AttnArgs &a, Lds &L, const int32_t *table, int x, int end,
                                                   uint64_t holes) {
@@ -99,13 +109,15 @@ struct Tiled {
       const int64_t row = place(a, table, x * KB + n, end);
       L.row[at * KB + n] = row < 0 ? 0 : row;
       const uint64_t there = __ballot(row >= 0);
-      const int lane = n & 63;
-      if (KB == 64 && lane == 0) L.present[at + n / KB] = there;
-      if (KB == 32 && lane % 32 == 0) L.present[at + n / KB] = there >> lane | 0xffffffff00000000ull;
+      if (n % 32 == 0) L.present[at * (KB / 32) + n / 32] = (uint32_t)(there >> (n & 32));
     }
     __syncthreads();
-    const uint64_t mine = __ballot(L.present[at + threadIdx.x % (kListed / 2)] != ~0ull) & 0xffffffffu;
-    return (holes & ~(0xffffffffull << at)) | mine << at;
+    bool hole = false;
+#pragma unroll
+    for (int u = 0; u < KB / 32; u++)
+      hole |= L.present[(at + threadIdx.x % (kListed / 2)) * (KB / 32) + u] != 0xffffffffu;
+    constexpr uint64_t kHalf = (1ull << kListed / 2) - 1;
+    return (holes & ~(kHalf << at)) | (__ballot(hole) & kHalf) << at;
   }
 
   // A copy of 16 bytes per lane from memory to LDS, in order from `to` on. The
@@ -117,11 +129,13 @@ struct Tiled {
                  : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to)), "v"(from)
                  : "memory");
   }
-  // This wave's loads of block x.
-  static __device__ __forceinline__ void fetch(const Lds &L, int x, const char *k, const char *v, lds_char *to,
+  // This wave's loads for turn x: keys of block x, values of block x - 1 (the
+  // first turn has none: block `lo`, which is listed).
+  static __device__ __forceinline__ void fetch(const Lds &L, int x, int lo, const char *k, const char *v, lds_char *to,
                                                uint32_t lane, int wave) {
     const uint32_t pos = lane % CH, sub = lane / CH;
-    const int64_t *rows = L.row + x % kListed * KB + sub;
+    const int64_t *key_rows = L.row + x % kListed * KB + sub;
+    const int64_t *value_rows = L.row + max(x - 1, lo) % kListed * KB + sub;
 #pragma unroll
     for (int i = 0; i < NL; i++) {
       const bool values = NL > 1 ? i & 1 : wave >= NW / 2;
@@ -130,7 +144,7 @@ struct Tiled {
       const int chunk = F8 ? 16 * pos
                            : values ? 16 * (pos ^ swizzle_v(sub)) ^ 16 * swizzle_v(first)
                                     : 16 * (pos ^ swizzle_k(sub)) ^ 16 * swizzle_k(first);
-      copy((values ? v : k) + rows[first] + chunk, to + (values ? KB * CH * 16 : 0) + group * 1024);
+      copy((values ? v + value_rows[first] : k + key_rows[first]) + chunk, to + (values ? KB * CH * 16 : 0) + group * 1024);
     }
   }
   // A block of e4m3 rows from LDS into LDS.
@@ -158,11 +172,12 @@ struct Tiled {
 
   // Values at places that are not there, and those that are not finite
   // numbers, set to zero (0 times NaN would reach rows that do not see them).
-  static __device__ __forceinline__ void make_finite(lds_char *v, uint64_t present, int *odd) {
+  static __device__ __forceinline__ void make_finite(lds_char *v, const uint32_t *present, int *odd) {
     bool lost = false;
     for (uint32_t x = threadIdx.x; x < kBlock / 16; x += kAttnThreads) {
       auto *p = (__attribute__((address_space(3))) u32x4 *)(v + 16 * x);
-      if (!((present >> (x / (ROW / 16))) & 1)) {
+      const uint32_t row = x / (ROW / 16);
+      if (!((present[row / 32] >> row % 32) & 1)) {
         *p = u32x4{0, 0, 0, 0};
         continue;
       }
@@ -182,24 +197,14 @@ struct Tiled {
     if (lost) *odd = 1;
   }
 
-  // The products of those values with the weights of the rows that see them;
-  // KT tiles of 32 places from k0 on.
-  template <int KT>
-  static __device__ __forceinline__ void add_not_finite(const AttnArgs &a, f32x16 *o, const float (*x)[16],
-                                                        const uint32_t *vis, const char *v, const int32_t *table,
-                                                        int k0, uint64_t present, int c, int h) {
-    for (int key = 0; key < 32 * KT; key++) {
-      if (!((present >> key) & 1)) continue;
-      const int at = (key >> 5) * 16 + ((key >> 3) & 3) * 4 + (key & 3);
-      float mine = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16 * KT; i++)
-        if (i == at) mine = x[i / 16][i % 16];
-      const float weight = __shfl(mine, c + 32 * ((key >> 2) & 1));
-      uint32_t word = vis[0];
-      if (KT > 1 && key >= 32) word = vis[KT - 1];
-      const bool sees = (word >> (key & 31)) & 1;
-      const char *row = v + place(a, table, k0 + key, INT32_MAX);
+  // Those values, at the places [p, end), to the rows that see them: whatever
+  // their weights were, the sums are then no finite numbers either.
+  static __device__ __forceinline__ void add_not_finite(const AttnArgs &a, f32x16 *o, const Request &rq, int node,
+                                                        const char *v, const int32_t *table, int p, int end, int h) {
+    for (; p < end; p++) {
+      const int64_t at = place(a, table, p, end);
+      if (at < 0 || !(seen(a, rq, node, p, 1) & 1)) continue;
+      const char *row = v + at;
 #pragma unroll
       for (int t = 0; t < DT; t++)
 #pragma unroll
@@ -212,59 +217,87 @@ struct Tiled {
             const uint32_t w = ((const uint16_t *)row)[d];
             y = not_finite2<BF>(w) & 0xffffu ? half_at<BF>(w, 0) : 0.f;
           }
-          if (sees && y != 0.f) o[t][i] += weight * y;
+          o[t][i] += y;
         }
     }
   }
 
-  // KT tiles of 32 places, from k0 on, for this wave's rows; keys: their rows
-  // in LDS. PARTIAL: with places that some rows do not see; from: the first
-  // such place.
-  template <bool PARTIAL, int KT>
-  static __device__ __forceinline__ void block(const AttnArgs &a, Wave &w, const Request &rq, int node, int k0,
-                                               int from, uint64_t present, float scale, lds_char *keys, bool odd,
-                                               const char *v, const int32_t *table, uint32_t lane) {
+  // The phase of products: VALUES: O += P V of the last block, SCORES: S = K Q
+  // of this one. buf: the wave's part of the turn's keys and values.
+  template <int KT>
+  static __device__ __forceinline__ void products(Wave<KT> &w, const lds_char *buf, bool values, bool scores,
+                                                  uint32_t lane) {
     typedef const __attribute__((address_space(3))) u32x4 *row_ptr;
     typedef __attribute__((address_space(3))) s16x4 *tr_ptr;
-    if (PARTIAL) asm volatile("" : "+v"(lane));  // nothing of this is kept in registers outside
     const int c = lane & 31, h = lane >> 5;
-    f32x16 s[KT];
-    {
-      const int f = h ^ swizzle_k(c);  // (the same for row c + 32)
-      const lds_char *row = keys + c * ROW;
+    const int fk = h ^ swizzle_k(c);  // (the same for rows c + 32 u)
+    const lds_char *keys = buf + c * ROW;
+    auto key = [&](int x) { return *(row_ptr)(keys + 16 * (2 * (x / KT) ^ fk) + 32 * (x % KT) * ROW); };
+    // lane i of a group of 16 reads row i / 4's values 4 (i % 4) + 0..3 of the
+    // group's 4 x 16 and receives column i's
+    const int i16 = lane & 15, row = 4 * h + i16 / 4, fv = swizzle_v(row);
+    const lds_char *vals = buf + kBlock + row * ROW + 8 * (i16 & 1);
+    auto value = [&](int x) {  // places 16 (x / DT) + 0..15, tile x % DT of the head
+      const lds_char *at =
+          vals + 16 * ((4 * (x % DT) + 2 * ((lane >> 4) & 1) + ((i16 >> 1) & 1)) ^ fv) + 16 * (x / DT) * ROW;
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)at));
+      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(at + 8 * ROW)));
+      return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    };
+    // reads stay kReads products ahead
+    constexpr int NK = NS * KT, NV = DT * 2 * KT, kReads = 4;
+    u32x4 k[kReads], vt[kReads];
+    if (values) {
 #pragma unroll
-      for (int u = 0; u < KT; u++) s[u] = f32x16{};
-      auto key = [&](int x) { return *(row_ptr)(row + 16 * (2 * (x / KT) ^ f) + 32 * (x % KT) * ROW); };
-      constexpr int N = NS * KT, kReads = 4;
-      u32x4 k[kReads];
+      for (int x = 0; x < kReads; x++) vt[x] = value(x);
+    }
 #pragma unroll
-      for (int x = 0; x < kReads; x++) k[x] = key(x);
+    for (int x = 0; x < kReads; x++) k[x] = key(x);
+    if (values) {
 #pragma unroll
-      for (int x = 0; x < N; x++) {
-        __builtin_amdgcn_sched_barrier(0);  // reads stay kReads products ahead
-        s[x % KT] = mfma32<BF>(k[x % kReads], w.q[x / KT], s[x % KT]);
-        if (x + kReads < N) k[x % kReads] = key(x + kReads);
+      for (int x = 0; x < NV; x++) {
+        __builtin_amdgcn_sched_barrier(0);
+        w.o[x % DT] = mfma32<BF>(vt[x % kReads], w.p[x / DT], w.o[x % DT]);
+        if (x + kReads < NV) vt[x % kReads] = value(x + kReads);
       }
     }
-    float x[KT][16];
-    uint32_t vis[KT];
+    if (scores) {
+#pragma unroll
+      for (int u = 0; u < KT; u++) w.s[u] = f32x16{};
+#pragma unroll
+      for (int x = 0; x < NK; x++) {
+        __builtin_amdgcn_sched_barrier(0);
+        w.s[x % KT] = mfma32<BF>(k[x % kReads], w.q[x / KT], w.s[x % KT]);
+        if (x + kReads < NK) k[x % kReads] = key(x + kReads);
+      }
+    }
+  }
+
+  // The scores of places that a row does not see, to minus infinity; from: the
+  // first place that some rows do not see.
+  template <int KT>
+  static __device__ __forceinline__ void hide(const AttnArgs &a, f32x16 *s, const Request &rq, int node, int k0,
+                                              int from, const uint32_t *present, uint32_t lane) {
+    const int h = lane >> 5;
 #pragma unroll
     for (int u = 0; u < KT; u++) {
+      uint32_t vis = present[u];
+      if (k0 + 32 * KT > from) vis = seen(a, rq, node, k0 + 32 * u, vis);
+      vis >>= 4 * h;
 #pragma unroll
-      for (int i = 0; i < 16; i++) x[u][i] = s[u][i];
-      if (PARTIAL) {
-        vis[u] = (uint32_t)(present >> (32 * u));
-        if (k0 + 32 * KT > from) vis[u] = seen(a, rq, node, k0 + 32 * u, vis[u]);
-#pragma unroll
-        for (int i = 0; i < 16; i++)
-          if (!((vis[u] >> (8 * (i / 4) + 4 * h + i % 4)) & 1)) x[u][i] = -INFINITY;
-      }
+      for (int i = 0; i < 16; i++)
+        if (!((vis >> (8 * (i / 4) + i % 4)) & 1)) s[u][i] = -INFINITY;
     }
-    float top = x[0][0];
+  }
+
+  // The phase of arithmetic: the scores become weights.
+  template <int KT>
+  static __device__ __forceinline__ void weights(Wave<KT> &w, float scale) {
+    float top = w.s[0][0];
 #pragma unroll
     for (int u = 0; u < KT; u++)
 #pragma unroll
-      for (int i = 0; i < 16; i++) top = fmaxf(top, x[u][i]);
+      for (int i = 0; i < 16; i++) top = fmaxf(top, w.s[u][i]);
     top *= scale;
     if (__ballot(top > w.ref + (kLift<BF> + kSlack))) {
       top = max_xor32(top) - kLift<BF>;
@@ -276,47 +309,16 @@ struct Tiled {
       for (int t = 0; t < DT; t++) w.o[t] *= keep;
     }
     const float ref = w.ref == -INFINITY ? 0.f : w.ref;
-    // lane i of a group of 16 reads row i / 4's values 4 (i % 4) + 0..3 of the
-    // group's 4 x 16 and receives column i's
-    const int i16 = lane & 15, key = 4 * h + i16 / 4, f = swizzle_v(key);
-    const lds_char *row = keys + kBlock + key * ROW + 8 * (i16 & 1);
-    auto value = [&](int j, int t) {  // places 16 j + 0..15, tile t of the head
-      const lds_char *at = row + 16 * ((4 * t + 2 * ((lane >> 4) & 1) + ((i16 >> 1) & 1)) ^ f) + 16 * j * ROW;
-      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)at));
-      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(at + 8 * ROW)));
-      return u32x4{lo[0], lo[1], hi[0], hi[1]};
-    };
-    // weight i of the 8 that product j takes from this lane
     float part[2] = {0.f, 0.f};
-    auto weight = [&](int j, int i, u32x4 &p) {
-      float *y = &x[j / 2][8 * (j & 1)];
-      y[i] = exp2_hw(fmaf(y[i], scale, -ref));
-      part[i & 1] += y[i];
-      if (i & 1) p[i / 2] = pack2<BF>(y[i - 1], y[i]);
-    };
-    constexpr int J = 2 * KT;
-    u32x4 p[2], vt[DT];
 #pragma unroll
-    for (int t = 0; t < DT; t++) vt[t] = value(0, t);
+    for (int u = 0; u < KT; u++)
 #pragma unroll
-    for (int i = 0; i < 8; i++) weight(0, i, p[0]);
-    // the products of one step beside the reads and the exponentials of the
-    // next, in this order
-#pragma unroll
-    for (int j = 0; j < J; j++)
-#pragma unroll
-      for (int t = 0; t < DT; t++) {
-        __builtin_amdgcn_sched_barrier(0);
-        w.o[t] = mfma32<BF>(vt[t], p[j & 1], w.o[t]);
-        if (j + 1 < J) {
-          vt[t] = value(j + 1, t);
-#pragma unroll
-          for (int i = 8 * t / DT; i < 8 * (t + 1) / DT; i++) weight(j + 1, i, p[(j + 1) & 1]);
-        }
+      for (int i = 0; i < 16; i++) {
+        w.s[u][i] = exp2_hw(fmaf(w.s[u][i], scale, -ref));
+        part[i & 1] += w.s[u][i];
+        if (i & 1) w.p[2 * u + i / 8][i % 8 / 2] = pack2<BF>(w.s[u][i - 1], w.s[u][i]);
       }
-    __builtin_amdgcn_sched_barrier(0);
     w.sum += part[0] + part[1];
-    if (PARTIAL && odd) add_not_finite<KT>(a, w.o, x, vis, v, table, k0, present, c, h);
   }
 
   // A tile's blocks [lo, hi): its result, or a partial one into `slot`.
@@ -331,7 +333,8 @@ struct Tiled {
     const int rows = rq.n * a.G, first_row = tile.row0 + first_in_tile, row = tile.row0 + in_tile;
     const bool on = row < rows, any = first_row < rows;
     const int node = on ? row / a.G : 0, hq = tile.h * a.G + (on ? row - node * a.G : 0);
-    Wave w;
+    constexpr int KT = PAIRED ? KB / 64 : KB / 32;
+    Wave<KT> w;
     // a negative scale turns the queries round, so that the largest product
     // has the largest score
     const uint32_t round = a.scale < 0.f ? 0x80008000u : 0u;
@@ -354,58 +357,85 @@ struct Tiled {
     const int from = a.mask || !any ? ctx : ctx + first_row / a.G + 1;
     const int until = !any ? 0 : a.mask ? rq.len : ctx + (min(first_row + 31, rows - 1)) / a.G + 1;
     const int end = min(hi * KB, rq.len);
-    constexpr int KT = PAIRED ? 1 : KB / 32;
-    const int half = PAIRED ? 32 * (wave & 1) : 0;
+    const int half = PAIRED ? 32 * KT * (wave & 1) : 0, late_wave = wave / (NW / 2);
     lds_char *buf = (lds_char *)L.buf, *ring = buf + kBuffers * kBuffer;
-    int cur = 0, raw = 0;  // the block in use, the ring's place that is fetched into
-    uint64_t holes = 0;    // blocks of the list with places that are not there
-    // Fetches block x and returns where the block to use is.
-    auto advance = [&](int x) {
-      lds_char *now = buf + cur * kBuffer;
+    int cur = 0, raw = 0;  // the turn's buffer, the ring's place that is fetched into
+    if (threadIdx.x == 0) L.odd = 0;
+    uint64_t holes = list(a, L, table, lo & -(kListed / 2), end, 0);  // blocks with places that are not there
+    // Begins turn j: fetches for a later one, and says where this one's keys
+    // and values are, and the next one's.
+    auto begin = [&](int j, const lds_char *&now, lds_char *&next) {
+      now = buf + cur * kBuffer + half * ROW;
       if constexpr (F8) {
-        fetch(L, x, k, v, ring + raw * kRaw, lane, wave);
+        fetch(L, j + kAhead, lo, k, v, ring + raw * kRaw, lane, wave);
         raw = raw + 1 == kRaws ? 0 : raw + 1;
-        widen(ring + raw * kRaw, buf + (1 - cur) * kBuffer);  // the oldest in the ring: the next to use
         cur = 1 - cur;
+        next = buf + cur * kBuffer;
+        widen(ring + raw * kRaw, next);  // the oldest in the ring
       } else {
-        fetch(L, x, k, v, buf + (cur == 0 ? kBuffers - 1 : cur - 1) * kBuffer, lane, wave);
+        fetch(L, j + kAhead, lo, k, v, buf + (cur == 0 ? kBuffers - 1 : cur - 1) * kBuffer, lane, wave);
         cur = cur + 1 == kBuffers ? 0 : cur + 1;
+        next = buf + cur * kBuffer;
       }
-      return now;
     };
-    holes = list(a, L, table, lo & -(kListed / 2), end, holes);
-    for (int j = lo - kAhead; j < hi; j++) {
-      // blocks that all rows see whole
-      if (j >= lo) {
-        const int next = (j + kAhead + kListed / 2 - 1) & -(kListed / 2);  // block to list from
-        const int whole = min(min(hi, max(tile_from, 0) / KB), next - kAhead);
-        for (; j < whole && !((holes >> (j % kListed)) & 1); j++) {
-          change_over<kInFlight>();
-          lds_char *now = advance(j + kAhead);
-          if (any)
-            block<false, KT>(a, w, rq, node, 0, 0, ~0ull, scale, now + half * ROW, false, v, table, lane);
+    auto hole = [&](int j) { return (holes >> (j % kListed)) & 1; };
+    auto whole = [&](int j) { return j * KB + KB <= tile_from && !hole(j); };
+    // The turns from j on whose block, and the one before, all rows see whole.
+    auto hot = [&](int j, auto late) {
+      const int next_list = (j + kAhead + kListed / 2 - 1) & -(kListed / 2);
+      const int stop = min(min(hi, max(tile_from, 0) / KB), next_list - kAhead);
+      for (; j < stop && !hole(j); j++) {
+        const lds_char *now;
+        lds_char *next;
+        change_over<kInFlight>();
+        begin(j, now, next);
+        if (any) {
+          if constexpr (late) weights<KT>(w, scale);
+          else products<KT>(w, now, true, true, lane);
         }
-        if (j >= hi) break;
-      }
-      const int k0 = j * KB;
-      change_over<kInFlight>();
-      if ((j + kAhead) % (kListed / 2) == 0 && j + kAhead > lo)
-        holes = list(a, L, table, j + kAhead, end, holes);
-      lds_char *now = advance(j + kAhead);
-      if (j < lo) continue;
-      const uint64_t present = in_all_lanes(L.present[j % kListed]);
-      bool odd = false;
-      if (k0 + KB > tile_from || present != ~0ull) {
-        if (threadIdx.x == 0) L.odd = 0;
         change_over<63>();
-        make_finite(now + kBlock, present, &L.odd);
-        change_over<63>();
-        odd = L.odd != 0;
+        if (any) {
+          if constexpr (late) products<KT>(w, now, true, true, lane);
+          else weights<KT>(w, scale);
+        }
       }
-      if (k0 + half < until)
-        block<true, KT>(a, w, rq, node, k0 + half, from, present >> half, scale, now + half * ROW, odd, v, table,
-                        lane);
-    }
+      return j;
+    };
+    auto turns = [&](auto late) {
+      for (int j = lo - kAhead; j <= hi; j++) {
+        if (j > lo && whole(j - 1)) {
+          j = hot(j, late);
+        }
+        // any other turn
+        uint32_t l = lane;
+        asm volatile("" : "+v"(l));  // nothing of this is kept in registers outside
+        const lds_char *now;
+        lds_char *next;
+        change_over<kInFlight>();
+        if ((j + kAhead) % (kListed / 2) == 0 && j + kAhead > lo) holes = list(a, L, table, j + kAhead, end, holes);
+        begin(j, now, next);
+        if (j < lo) continue;
+        if (j < hi && !whole(j)) {
+          change_over<F8 ? 63 : NL>();
+          make_finite(next + kBlock, L.present + j % kListed * (KB / 32), &L.odd);
+          change_over<63>();
+        }
+        auto use = [&](int j) { return j >= lo && j < hi && j * KB + half < until; };
+        for (int phase = 0; phase < 2; phase++) {
+          if (phase) change_over<63>();
+          const int of = late && !phase ? j - 1 : j;  // whose arithmetic
+          if (phase == late) products<KT>(w, now, use(j - 1), use(j), l);
+          else if (use(of)) {
+            if (!whole(of))
+              hide<KT>(a, w.s, rq, node, of * KB + half, from, L.present + (of % kListed * KB + half) / 32, l);
+            weights<KT>(w, scale);
+          }
+        }
+      }
+    };
+    if (late_wave) turns(std::true_type{});
+    else turns(std::false_type{});
+    const bool odd = L.odd != 0;
     change_over<0>();  // LDS is free
     float sum = sum_xor32(w.sum);
     if constexpr (PAIRED) {
@@ -433,6 +463,7 @@ struct Tiled {
       if (wave & 1) return;
     }
     if (!on) return;
+    if (odd) add_not_finite(a, w.o, rq, node, v, table, lo * KB, end, h);
     if (slot < 0) {
       const float f = sum == 0.f ? 0.f : (a.c.v_scale ? a.c.v_scale[tile.h] : 1.f) / sum;
       const size_t tok = rq.t0 + node;
@@ -466,8 +497,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnArgs a) 
   using S = Tiled<BF, F8, D>;
   __shared__ typename S::Lds L;
   walk<S::RT, S::KB, kPairedRows<D>, D, kAttnThreads>(a, [&](const Tile &tile, int lo, int hi, int slot) {
-    if (kPairedRows<D> && tile.rows <= kPairedRows<D>) S::template segment<true>(a, L, tile, lo, hi, slot, gridDim.x);
-    else S::template segment<false>(a, L, tile, lo, hi, slot, gridDim.x);
+    if constexpr (kPairedRows<D> > 0) {
+      if (tile.rows <= kPairedRows<D>) return S::template segment<true>(a, L, tile, lo, hi, slot, gridDim.x);
+    }
+    S::template segment<false>(a, L, tile, lo, hi, slot, gridDim.x);
   });
 }
 
