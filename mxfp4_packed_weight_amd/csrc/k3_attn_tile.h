@@ -60,6 +60,7 @@ struct Tiled {
   static constexpr int CH = D * ES / 16;             // chunks of a row of the cache
   static constexpr int RPL = 64 / CH;                // rows per load of a wave
   static constexpr int NL = 2 * KB / RPL / NW;       // loads of a wave, keys and values
+  static constexpr int NR = (NL + 1) / 2;            // rows of a lane in them
   static constexpr int kBlock = KB * ROW, kBuffer = 2 * kBlock, kRaw = 2 * KB * D;
   static constexpr int kAhead = F8 ? 3 : 2;
   static constexpr int kBuffers = F8 ? 2 : kAhead + 1, kRaws = F8 ? kAhead : 0;
@@ -129,22 +130,46 @@ struct Tiled {
                  : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to)), "v"(from)
                  : "memory");
   }
-  // This wave's loads for turn x: keys of block x, values of block x - 1 (the
-  // first turn has none: block `lo`, which is listed).
-  static __device__ __forceinline__ void fetch(const Lds &L, int x, int lo, const char *k, const char *v, lds_char *to,
-                                               uint32_t lane, int wave) {
+  // Where the rows are that a wave loads in a turn: keys of block x, values of
+  // block x - 1 (the first turn has none: block `lo`, which is listed).
+  struct Rows {
+    int64_t key[NR], value[NR];
+  };
+  static __device__ __forceinline__ const int64_t *listed(const Lds &L, int x, int i, uint32_t lane, int wave) {
+    const int group = NL > 1 ? wave * NR + i : wave % (NW / 2);
+    return L.row + x % kListed * KB + group * RPL + lane / CH;
+  }
+  static __device__ __forceinline__ Rows rows_of(const Lds &L, int x, int lo, uint32_t lane, int wave) {
+    Rows r;
+#pragma unroll
+    for (int i = 0; i < NR; i++) {
+      r.key[i] = *listed(L, x, i, lane, wave);
+      r.value[i] = *listed(L, max(x - 1, lo), i, lane, wave);
+    }
+    return r;
+  }
+  // (block x may not be listed yet: then these rows are not used)
+  static __device__ __forceinline__ Rows rows_after(const Lds &L, const Rows &now, int x, uint32_t lane, int wave) {
+    Rows r;
+#pragma unroll
+    for (int i = 0; i < NR; i++) {
+      r.key[i] = *listed(L, x, i, lane, wave);
+      r.value[i] = now.key[i];
+    }
+    return r;
+  }
+  static __device__ __forceinline__ void fetch(const Rows &r, const char *k, const char *v, lds_char *to, uint32_t lane,
+                                               int wave) {
     const uint32_t pos = lane % CH, sub = lane / CH;
-    const int64_t *key_rows = L.row + x % kListed * KB + sub;
-    const int64_t *value_rows = L.row + max(x - 1, lo) % kListed * KB + sub;
 #pragma unroll
     for (int i = 0; i < NL; i++) {
       const bool values = NL > 1 ? i & 1 : wave >= NW / 2;
-      const int group = NL > 1 ? wave * (NL / 2) + i / 2 : wave % (NW / 2), first = group * RPL;
+      const int group = NL > 1 ? wave * NR + i / 2 : wave % (NW / 2), first = group * RPL;
       // (the swizzles are linear in the bits of the row)
       const int chunk = F8 ? 16 * pos
                            : values ? 16 * (pos ^ swizzle_v(sub)) ^ 16 * swizzle_v(first)
                                     : 16 * (pos ^ swizzle_k(sub)) ^ 16 * swizzle_k(first);
-      copy((values ? v + value_rows[first] : k + key_rows[first]) + chunk, to + (values ? KB * CH * 16 : 0) + group * 1024);
+      copy((values ? v + r.value[i / 2] : k + r.key[i / 2]) + chunk, to + (values ? KB * CH * 16 : 0) + group * 1024);
     }
   }
   // A block of e4m3 rows from LDS into LDS.
@@ -247,6 +272,7 @@ struct Tiled {
     // reads stay kReads products ahead
     constexpr int NK = NS * KT, NV = DT * 2 * KT, kReads = 4;
     u32x4 k[kReads], vt[kReads];
+    __builtin_amdgcn_s_setprio(1);
     if (values) {
 #pragma unroll
       for (int x = 0; x < kReads; x++) vt[x] = value(x);
@@ -271,6 +297,7 @@ struct Tiled {
         if (x + kReads < NK) k[x % kReads] = key(x + kReads);
       }
     }
+    __builtin_amdgcn_s_setprio(0);
   }
 
   // The scores of places that a row does not see, to minus infinity; from: the
@@ -362,18 +389,18 @@ struct Tiled {
     int cur = 0, raw = 0;  // the turn's buffer, the ring's place that is fetched into
     if (threadIdx.x == 0) L.odd = 0;
     uint64_t holes = list(a, L, table, lo & -(kListed / 2), end, 0);  // blocks with places that are not there
-    // Begins turn j: fetches for a later one, and says where this one's keys
-    // and values are, and the next one's.
-    auto begin = [&](int j, const lds_char *&now, lds_char *&next) {
+    // Begins turn j: fetches `rows` for a later one, and says where this one's
+    // keys and values are, and the next one's.
+    auto begin = [&](const Rows &rows, const lds_char *&now, lds_char *&next) {
       now = buf + cur * kBuffer + half * ROW;
       if constexpr (F8) {
-        fetch(L, j + kAhead, lo, k, v, ring + raw * kRaw, lane, wave);
+        fetch(rows, k, v, ring + raw * kRaw, lane, wave);
         raw = raw + 1 == kRaws ? 0 : raw + 1;
         cur = 1 - cur;
         next = buf + cur * kBuffer;
         widen(ring + raw * kRaw, next);  // the oldest in the ring
       } else {
-        fetch(L, j + kAhead, lo, k, v, buf + (cur == 0 ? kBuffers - 1 : cur - 1) * kBuffer, lane, wave);
+        fetch(rows, k, v, buf + (cur == 0 ? kBuffers - 1 : cur - 1) * kBuffer, lane, wave);
         cur = cur + 1 == kBuffers ? 0 : cur + 1;
         next = buf + cur * kBuffer;
       }
@@ -384,11 +411,13 @@ struct Tiled {
     auto hot = [&](int j, auto late) {
       const int next_list = (j + kAhead + kListed / 2 - 1) & -(kListed / 2);
       const int stop = min(min(hi, max(tile_from, 0) / KB), next_list - kAhead);
+      Rows rows = rows_of(L, j + kAhead, lo, lane, wave);
       for (; j < stop && !hole(j); j++) {
         const lds_char *now;
         lds_char *next;
         change_over<kInFlight>();
-        begin(j, now, next);
+        begin(rows, now, next);
+        rows = rows_after(L, rows, j + 1 + kAhead, lane, wave);
         if (any) {
           if constexpr (late) weights<KT>(w, scale);
           else products<KT>(w, now, true, true, lane);
@@ -413,7 +442,7 @@ struct Tiled {
         lds_char *next;
         change_over<kInFlight>();
         if ((j + kAhead) % (kListed / 2) == 0 && j + kAhead > lo) holes = list(a, L, table, j + kAhead, end, holes);
-        begin(j, now, next);
+        begin(rows_of(L, j + kAhead, lo, lane, wave), now, next);
         if (j < lo) continue;
         if (j < hi && !whole(j)) {
           change_over<F8 ? 63 : NL>();
