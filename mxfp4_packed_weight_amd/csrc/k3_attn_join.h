@@ -1,18 +1,20 @@
 // Joins the tiles that were split: workgroup b's is the tile that begins in
-// its stretch of the line and goes on in the next ones. A wave joins one row
-// at a time, four values per lane, as many parts side by side as lanes allow
-// and eight of those in flight: maxima, sums and values of a step's parts are
-// loaded together, so a row costs one memory latency per step (the parts are
-// few and come from other dies' memory; latency is all that this launch has).
+// its stretch of the line and goes on in the next ones. The parts come from
+// other dies' memory, and latency is all that this launch has: loads of
+// several rows or parts go out together. Tiles in few parts: four values of
+// four rows per thread, part by part. Tiles in many (long rows of few
+// requests): a wave per row, as many parts side by side as lanes allow and
+// eight of those in flight.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "k3_attn.h"
 
 namespace k3 {
 
-constexpr int kJoinWaves = 4;
+constexpr int kJoinWaves = 4, kFewParts = 6;
 
 template <bool BF, int D>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, int B) {
@@ -20,7 +22,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
   const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const JoinJob *jobs = join_jobs<D>(a, B);
   const JoinJob job = jobs[b];
-  if ((int)blockIdx.y * kJoinWaves + wave >= job.rows) return;
+  if (job.rows == 0) return;
   int *slots = lists[wave], n = 0;
   for (int x0 = b; x0 <= job.last; x0 += 64) {
     const int x = x0 + lane;
@@ -32,11 +34,55 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
   wave_sync();
   if (n == 0) return;  // one workgroup had all of its blocks
   constexpr int LPR = D / 4, SIDE = 64 / LPR;
-  const int sub = lane / LPR, d = lane % LPR * 4;
+  const int d = lane % LPR * 4;
+  auto weight = [&](float m, float top) { return m == top ? 1.f : exp2_hw(m - top); };
+  auto store = [&](int r, float ref, float sum, f32x4 o) {
+    const int row = job.row0 + r, i = row / a.G, hq = job.h * a.G + row - i * a.G;
+    const size_t tok = job.t0 + i;
+    const float f = sum == 0.f ? 0.f : (a.c.v_scale ? a.c.v_scale[job.h] : 1.f) / sum;
+    *(u32x2 *)(a.out + tok * a.out_stride + hq * D + d) =
+        u32x2{pack2<BF>(o[0] * f, o[1] * f), pack2<BF>(o[2] * f, o[3] * f)};
+    if (a.lse && d == 0) a.lse[tok * a.Hq + hq] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+  };
+  if (n <= kFewParts) {
+    constexpr int ROWS = 4, PASS = 64 * kJoinWaves / LPR;  // rows of a thread, rows side by side
+    for (int r0 = blockIdx.y * ROWS * PASS; r0 < job.rows; r0 += gridDim.y * ROWS * PASS) {
+      float ref[ROWS], sum[ROWS];
+      f32x4 o[ROWS];
+#pragma unroll 2
+      for (int x = 0; x < n; x++) {
+        const int slot = __builtin_amdgcn_readfirstlane(slots[x]);
+        const float *ml = part_ml<D>(a, B, slot), *po = part_o<D>(a, slot, 0) + d;
+        float m[ROWS], s[ROWS];
+        f32x4 p[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; i++) {
+          const int r = min(r0 + i * PASS + (int)threadIdx.x / LPR, job.rows - 1);
+          m[i] = ml[r];
+          s[i] = ml[a.part_rows + r];
+          p[i] = *(const f32x4 *)(po + r * D);
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; i++) {
+          const float top = x ? fmaxf(ref[i], m[i]) : m[i];
+          const float mine = x ? weight(ref[i], top) : 0.f, other = weight(m[i], top);
+          sum[i] = x ? sum[i] * mine + s[i] * other : s[i];
+          o[i] = x ? o[i] * mine + p[i] * other : p[i];
+          ref[i] = top;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < ROWS; i++) {
+        const int r = r0 + i * PASS + (int)threadIdx.x / LPR;
+        if (r < job.rows) store(r, ref[i], sum[i], o[i]);
+      }
+    }
+    return;
+  }
+  const int sub = lane / LPR;
   for (int r = blockIdx.y * kJoinWaves + wave; r < job.rows; r += gridDim.y * kJoinWaves) {
     float ref = -INFINITY, sum = 0.f;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    auto weight = [&](float m, float top) { return m == top ? 1.f : exp2_hw(m - top); };
     auto join = [&](auto ahead, int x0) {
       constexpr int kAhead = decltype(ahead)::value;
       f32x4 p[kAhead];
@@ -76,14 +122,18 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
 #pragma unroll
       for (int i = 0; i < 4; i++) o[i] = o[i] * mine + __shfl_xor(o[i], k) * other;
     }
-    if (sub) continue;
-    const int row = job.row0 + r, i = row / a.G, hq = job.h * a.G + row - i * a.G;
-    const size_t tok = job.t0 + i;
-    const float f = sum == 0.f ? 0.f : (a.c.v_scale ? a.c.v_scale[job.h] : 1.f) / sum;
-    *(u32x2 *)(a.out + tok * a.out_stride + hq * D + d) =
-        u32x2{pack2<BF>(o[0] * f, o[1] * f), pack2<BF>(o[2] * f, o[3] * f)};
-    if (a.lse && lane == 0) a.lse[tok * a.Hq + hq] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+    if (sub == 0) store(r, ref, sum, o);
   }
+}
+
+// Workgroups to a tile: enough for its rows in few parts, and for the card
+// where there are few tiles.
+template <int D>
+inline int join_height(const AttnArgs &a, int B) {
+  const long long tiles = (long long)a.R * (((long long)a.T * a.G + a.R * 256ll - 1) / (a.R * 256ll)) * a.c.n_heads;
+  const int few = (a.part_rows * D / 16 + 64 * kJoinWaves - 1) / (64 * kJoinWaves);
+  const int most = (a.part_rows + kJoinWaves - 1) / kJoinWaves;
+  return std::min(most, std::max(few, (int)(2048 / std::min<long long>(tiles, B))));
 }
 
 }  // namespace k3

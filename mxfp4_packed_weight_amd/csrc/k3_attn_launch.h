@@ -1,8 +1,6 @@
 // Which attention kernel a call takes, and its launches.
 #pragma once
 
-#include <algorithm>
-
 #include "k3_attn_join.h"
 #include "k3_attn_stream.h"
 #include "k3_attn_tile.h"
@@ -12,7 +10,7 @@ namespace k3 {
 template <bool BF, int D>
 hipError_t launch_join(const AttnArgs &a, int B, hipStream_t s) {
   if (const hipError_t e = hipGetLastError()) return e;
-  attn_join_kernel<BF, D><<<dim3(B, std::min((a.part_rows + kJoinWaves - 1) / kJoinWaves, 32)), 64 * kJoinWaves, 0, s>>>(a, B);
+  attn_join_kernel<BF, D><<<dim3(B, join_height<D>(a, B)), 64 * kJoinWaves, 0, s>>>(a, B);
   return hipGetLastError();
 }
 
