@@ -34,6 +34,10 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 // A block for a tile of up to half the waves' rows takes 10 / 16 of the time
 // of a full one.
 constexpr int kHalfCost = 10;
+// A tile's fixed cost, in blocks: its tables, queries and first blocks come
+// one after the other (about 10 us), and its results go out.
+template <int RT>
+constexpr int kFixedBlocks = RT < 128 ? 1 : 6;
 constexpr int kMaxWorkgroups = 1024;  // of a launch: at most two to a CU
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The running maximum is raised only by more than this (in powers of two):
@@ -68,7 +72,7 @@ template <int RT, int KB, int HALF>
 struct Cost {
   int tiles, last_rows;
   long long base, slope, all;
-  static constexpr long long kFixed = 16 * KB;  // queries in, results out
+  static constexpr long long kFixed = 16 * KB * kFixedBlocks<RT>;  // queries in, results out
   __device__ __forceinline__ Cost(const AttnArgs &a, const Request &q) {
     const long long rows = (long long)q.n * a.G;
     tiles = (int)((rows + RT - 1) / RT);
@@ -171,12 +175,12 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &
 }
 
 // The tile's first block that is done after place u of the line.
-template <int KB>
+template <int RT, int KB>
 __device__ __forceinline__ int block_from(const Tile &t, long long u) {
   if (u <= t.first) return 0;
   if (u >= t.after) return t.blocks;
-  const int each = KB * t.weight;  // a block's cost; as much is fixed
-  const long long y = max(u - t.first - each, 0ll);
+  const int each = KB * t.weight;  // a block's cost
+  const long long y = max(u - t.first - each * kFixedBlocks<RT>, 0ll);
   return (int)min((y + each - 1) / each, (long long)t.blocks);
 }
 
@@ -228,7 +232,7 @@ __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
   JoinJob job = {0, 0, 0, 0, -1, -1, -1, 0};
   for (long long u = begin; u < end;) {
     const Tile tile = tile_at<RT, KB, HALF>(a, L, u);
-    const int lo = block_from<KB>(tile, u), hi = block_from<KB>(tile, end);
+    const int lo = block_from<RT, KB>(tile, u), hi = block_from<RT, KB>(tile, end);
     const int slot = lo == hi || (lo == 0 && hi == tile.blocks) ? -1 : lo ? 2 * b : 2 * b + 1;
     if (u > tile.first) job.head_slot = slot;
     else if (tile.after > end) {

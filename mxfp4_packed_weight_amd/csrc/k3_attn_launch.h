@@ -23,14 +23,14 @@ hipError_t launch_stream(const AttnArgs &a, hipStream_t s) {
 
 template <bool BF, bool F8, int D>
 hipError_t launch_tile(const AttnArgs &a, hipStream_t s) {
-  const int B = attn_workgroups(kAttnRows);
-  attn_tile_kernel<BF, F8, D><<<B, kAttnThreads, 0, s>>>(a);
+  const int B = attn_workgroups(32 * kAttnWaves<D>);
+  attn_tile_kernel<BF, F8, D><<<B, kAttnThreads<D>, 0, s>>>(a);
   return launch_join<BF, D>(a, B, s);
 }
 
 template <bool BF, bool F8, int D>
 hipError_t launch_attn(const AttnArgs &a, hipStream_t s) {
-  switch (attn_tile_rows(a.T, a.G, a.R)) {
+  switch (attn_tile_rows(a.T, a.G, a.R, D)) {
     case 16: return launch_stream<BF, F8, D, 1>(a, s);
     case 32: return launch_stream<BF, F8, D, 2>(a, s);
     default: return launch_tile<BF, F8, D>(a, s);

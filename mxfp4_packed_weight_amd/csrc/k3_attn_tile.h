@@ -12,7 +12,9 @@
 // ones into a ring of their own, and widened from there one turn ahead, once
 // for all waves). A tile of up to 128 rows would leave half of the waves
 // without work: there, two waves share 32 rows, each has half of every block,
-// and they join their results at the end.
+// and they join their results at the end. A head of 256 needs the registers of
+// two waves: four waves, each with a SIMD to itself, whose products run beside
+// its own exponentials.
 // As in the streaming kernel all is transposed (lane l, c = l % 32, h = l / 32):
 //   S^T = K Q^T   rows: 32 places, columns: the wave's 32 rows. The lane has
 //                 row c's scores of places 8 b + 4 h + 0..3.
@@ -44,16 +46,20 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c) {
                                                 0);
 }
 
-constexpr int kAttnWaves = 8, kAttnRows = 32 * kAttnWaves, kAttnThreads = 64 * kAttnWaves;
+template <int D>
+constexpr int kAttnWaves = D == 256 ? 4 : 8;
+template <int D>
+constexpr int kAttnThreads = 64 * kAttnWaves<D>;
 template <int D>
 constexpr int kAttnKeys = D == 256 ? 32 : 64;
 // Tiles of so many rows go two waves to 32 rows (not with blocks of 32).
 template <int D>
-constexpr int kPairedRows = kAttnKeys<D> >= 64 ? kAttnRows / 2 : 0;
+constexpr int kPairedRows = D == 256 ? 0 : 128;
 
 template <bool BF, bool F8, int D>
 struct Tiled {
-  static constexpr int NW = kAttnWaves, RT = kAttnRows, KB = kAttnKeys<D>;
+  static constexpr int NW = kAttnWaves<D>, RT = 32 * NW, KB = kAttnKeys<D>, kThreads = kAttnThreads<D>;
+  static constexpr bool kPhases = NW == 8;           // two waves to a SIMD, a phase apart
   static constexpr int NS = D / 16, DT = D / 32;     // steps over the head, tiles of the output
   static constexpr int ROW = 2 * D;                  // a row of LDS, D / 8 chunks
   static constexpr int ES = F8 ? 1 : 2;
@@ -105,8 +111,8 @@ struct Tiled {
                                                   uint64_t holes) {
     const int at = x % kListed;
 #pragma unroll
-    for (int i = 0; i < kListed / 2 * KB / kAttnThreads; i++) {
-      const int n = i * kAttnThreads + threadIdx.x;
+    for (int i = 0; i < kListed / 2 * KB / kThreads; i++) {
+      const int n = i * kThreads + threadIdx.x;
       const int64_t row = place(a, table, x * KB + n, end);
       L.row[at * KB + n] = row < 0 ? 0 : row;
       const uint64_t there = __ballot(row >= 0);
@@ -178,8 +184,8 @@ struct Tiled {
       return u32x4{widen2<BF, false>(x), widen2<BF, true>(x), widen2<BF, false>(y), widen2<BF, true>(y)};
     };
 #pragma unroll
-    for (int i = 0; i < kRaw / 16 / kAttnThreads; i++) {
-      const int x = i * kAttnThreads + threadIdx.x;  // a chunk: two of the wide row
+    for (int i = 0; i < kRaw / 16 / kThreads; i++) {
+      const int x = i * kThreads + threadIdx.x;  // a chunk: two of the wide row
       const int row = x / CH, chunk = 2 * (x % CH);
       const u32x4 w = *(const __attribute__((address_space(3))) u32x4 *)(from + 16 * x);
       const int f = row < KB ? swizzle_k(row) : swizzle_v(row);
@@ -199,7 +205,7 @@ struct Tiled {
   // numbers, set to zero (0 times NaN would reach rows that do not see them).
   static __device__ __forceinline__ void make_finite(lds_char *v, const uint32_t *present, int *odd) {
     bool lost = false;
-    for (uint32_t x = threadIdx.x; x < kBlock / 16; x += kAttnThreads) {
+    for (uint32_t x = threadIdx.x; x < kBlock / 16; x += kThreads) {
       auto *p = (__attribute__((address_space(3))) u32x4 *)(v + 16 * x);
       const uint32_t row = x / (ROW / 16);
       if (!((present[row / 32] >> row % 32) & 1)) {
@@ -247,57 +253,75 @@ struct Tiled {
     }
   }
 
-  // The phase of products: VALUES: O += P V of the last block, SCORES: S = K Q
-  // of this one. buf: the wave's part of the turn's keys and values.
+  // Reads of operands from a turn's keys and values.
+  template <int KT>
+  struct Reader {
+    const lds_char *keys, *vals;
+    int fk, fv, column;
+    __device__ __forceinline__ Reader(const lds_char *buf, uint32_t lane) {
+      const int c = lane & 31, h = lane >> 5;
+      keys = buf + c * ROW;
+      fk = h ^ swizzle_k(c);  // (the same for rows c + 32 u)
+      // lane i of a group of 16 reads row i / 4's values 4 (i % 4) + 0..3 of the
+      // group's 4 x 16 and receives column i's
+      const int i16 = lane & 15, row = 4 * h + i16 / 4;
+      vals = buf + kBlock + row * ROW + 8 * (i16 & 1);
+      fv = swizzle_v(row);
+      column = 2 * ((lane >> 4) & 1) + ((i16 >> 1) & 1);
+    }
+    // step x / KT over the head, 32 places from 32 (x % KT) on
+    __device__ __forceinline__ u32x4 key(int x) const {
+      typedef const __attribute__((address_space(3))) u32x4 *ptr;
+      return *(ptr)(keys + 16 * (2 * (x / KT) ^ fk) + 32 * (x % KT) * ROW);
+    }
+    // places 16 (x / DT) + 0..15, tile x % DT of the head
+    __device__ __forceinline__ u32x4 value(int x) const {
+      typedef __attribute__((address_space(3))) s16x4 *ptr;
+      const lds_char *at = vals + 16 * ((4 * (x % DT) + column) ^ fv) + 16 * (x / DT) * ROW;
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)at));
+      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(at + 8 * ROW)));
+      return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+  };
+  static constexpr int kReads = 4;  // products that the reads are ahead
+  template <int KT>
+  static __device__ __forceinline__ void scores_of(Wave<KT> &w, const Reader<KT> &in, u32x4 *k) {
+    constexpr int N = NS * KT;
+#pragma unroll
+    for (int u = 0; u < KT; u++) w.s[u] = f32x16{};
+#pragma unroll
+    for (int x = 0; x < N; x++) {
+      __builtin_amdgcn_sched_barrier(0);
+      w.s[x % KT] = mfma32<BF>(k[x % kReads], w.q[x / KT], w.s[x % KT]);
+      if (x + kReads < N) k[x % kReads] = in.key(x + kReads);
+    }
+  }
+
+  // The phase of products: `values`: O += P V of the last block, `scores`:
+  // S = K Q of this one. buf: the wave's part of the turn's keys and values.
   template <int KT>
   static __device__ __forceinline__ void products(Wave<KT> &w, const lds_char *buf, bool values, bool scores,
                                                   uint32_t lane) {
-    typedef const __attribute__((address_space(3))) u32x4 *row_ptr;
-    typedef __attribute__((address_space(3))) s16x4 *tr_ptr;
-    const int c = lane & 31, h = lane >> 5;
-    const int fk = h ^ swizzle_k(c);  // (the same for rows c + 32 u)
-    const lds_char *keys = buf + c * ROW;
-    auto key = [&](int x) { return *(row_ptr)(keys + 16 * (2 * (x / KT) ^ fk) + 32 * (x % KT) * ROW); };
-    // lane i of a group of 16 reads row i / 4's values 4 (i % 4) + 0..3 of the
-    // group's 4 x 16 and receives column i's
-    const int i16 = lane & 15, row = 4 * h + i16 / 4, fv = swizzle_v(row);
-    const lds_char *vals = buf + kBlock + row * ROW + 8 * (i16 & 1);
-    auto value = [&](int x) {  // places 16 (x / DT) + 0..15, tile x % DT of the head
-      const lds_char *at =
-          vals + 16 * ((4 * (x % DT) + 2 * ((lane >> 4) & 1) + ((i16 >> 1) & 1)) ^ fv) + 16 * (x / DT) * ROW;
-      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)at));
-      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)(at + 8 * ROW)));
-      return u32x4{lo[0], lo[1], hi[0], hi[1]};
-    };
-    // reads stay kReads products ahead
-    constexpr int NK = NS * KT, NV = DT * 2 * KT, kReads = 4;
+    const Reader<KT> in(buf, lane);
+    constexpr int N = DT * 2 * KT;
     u32x4 k[kReads], vt[kReads];
-    __builtin_amdgcn_s_setprio(1);
+    if (kPhases) __builtin_amdgcn_s_setprio(1);
     if (values) {
 #pragma unroll
-      for (int x = 0; x < kReads; x++) vt[x] = value(x);
+      for (int x = 0; x < kReads; x++) vt[x] = in.value(x);
     }
 #pragma unroll
-    for (int x = 0; x < kReads; x++) k[x] = key(x);
+    for (int x = 0; x < kReads; x++) k[x] = in.key(x);
     if (values) {
 #pragma unroll
-      for (int x = 0; x < NV; x++) {
+      for (int x = 0; x < N; x++) {
         __builtin_amdgcn_sched_barrier(0);
         w.o[x % DT] = mfma32<BF>(vt[x % kReads], w.p[x / DT], w.o[x % DT]);
-        if (x + kReads < NV) vt[x % kReads] = value(x + kReads);
+        if (x + kReads < N) vt[x % kReads] = in.value(x + kReads);
       }
     }
-    if (scores) {
-#pragma unroll
-      for (int u = 0; u < KT; u++) w.s[u] = f32x16{};
-#pragma unroll
-      for (int x = 0; x < NK; x++) {
-        __builtin_amdgcn_sched_barrier(0);
-        w.s[x % KT] = mfma32<BF>(k[x % kReads], w.q[x / KT], w.s[x % KT]);
-        if (x + kReads < NK) k[x % kReads] = key(x + kReads);
-      }
-    }
-    __builtin_amdgcn_s_setprio(0);
+    if (scores) scores_of<KT>(w, in, k);
+    if (kPhases) __builtin_amdgcn_s_setprio(0);
   }
 
   // The scores of places that a row does not see, to minus infinity; from: the
@@ -317,20 +341,37 @@ struct Tiled {
     }
   }
 
-  // The phase of arithmetic: the scores become weights.
+  // The reference exponent for the new scores; true if it rose (in any lane),
+  // and `keep`, what the old sums are worth then.
   template <int KT>
-  static __device__ __forceinline__ void weights(Wave<KT> &w, float scale) {
+  static __device__ __forceinline__ bool raise(Wave<KT> &w, float scale, float &keep) {
     float top = w.s[0][0];
 #pragma unroll
     for (int u = 0; u < KT; u++)
 #pragma unroll
       for (int i = 0; i < 16; i++) top = fmaxf(top, w.s[u][i]);
     top *= scale;
-    if (__ballot(top > w.ref + (kLift<BF> + kSlack))) {
-      top = max_xor32(top) - kLift<BF>;
-      const float ref = fmaxf(w.ref, top);
-      const float keep = w.ref == ref ? 1.f : exp2_hw(w.ref - ref);
-      w.ref = ref;
+    if (!__ballot(top > w.ref + (kLift<BF> + kSlack))) return false;
+    top = max_xor32(top) - kLift<BF>;
+    const float ref = fmaxf(w.ref, top);
+    keep = w.ref == ref ? 1.f : exp2_hw(w.ref - ref);
+    w.ref = ref;
+    return true;
+  }
+  // Weight i of the lane's, and its part in the sum.
+  template <int KT>
+  static __device__ __forceinline__ void weight(Wave<KT> &w, u32x4 *p, int i, float scale, float ref, float *part) {
+    f32x16 &x = w.s[i / 16];
+    x[i % 16] = exp2_hw(fmaf(x[i % 16], scale, -ref));
+    part[i & 1] += x[i % 16];
+    if (i & 1) p[i / 8][i % 8 / 2] = pack2<BF>(x[i % 16 - 1], x[i % 16]);
+  }
+
+  // The phase of arithmetic: the scores become weights.
+  template <int KT>
+  static __device__ __forceinline__ void weights(Wave<KT> &w, float scale) {
+    float keep;
+    if (raise<KT>(w, scale, keep)) {
       w.sum *= keep;
 #pragma unroll
       for (int t = 0; t < DT; t++) w.o[t] *= keep;
@@ -338,14 +379,43 @@ struct Tiled {
     const float ref = w.ref == -INFINITY ? 0.f : w.ref;
     float part[2] = {0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < KT; u++)
-#pragma unroll
-      for (int i = 0; i < 16; i++) {
-        w.s[u][i] = exp2_hw(fmaf(w.s[u][i], scale, -ref));
-        part[i & 1] += w.s[u][i];
-        if (i & 1) w.p[2 * u + i / 8][i % 8 / 2] = pack2<BF>(w.s[u][i - 1], w.s[u][i]);
-      }
+    for (int i = 0; i < 16 * KT; i++) weight<KT>(w, w.p, i, scale, ref, part);
     w.sum += part[0] + part[1];
+  }
+
+  // Both, for a wave that has its SIMD to itself: this block's scores, then
+  // the last block's values beside this one's exponentials.
+  template <int KT>
+  static __device__ __forceinline__ void both(Wave<KT> &w, const lds_char *buf, float scale, uint32_t lane) {
+    const Reader<KT> in(buf, lane);
+    u32x4 k[kReads], vt[kReads], p[2 * KT];
+#pragma unroll
+    for (int x = 0; x < kReads; x++) k[x] = in.key(x);
+    scores_of<KT>(w, in, k);
+#pragma unroll
+    for (int x = 0; x < kReads; x++) vt[x] = in.value(x);
+    float keep, part[2] = {0.f, 0.f};
+    const bool rose = raise<KT>(w, scale, keep);
+    const float ref = w.ref == -INFINITY ? 0.f : w.ref;
+    constexpr int N = DT * 2 * KT, kEach = 16 * KT / N;
+    static_assert(kEach >= 1, "");
+#pragma unroll
+    for (int x = 0; x < N; x++) {
+      __builtin_amdgcn_sched_barrier(0);
+      w.o[x % DT] = mfma32<BF>(vt[x % kReads], w.p[x / DT], w.o[x % DT]);
+      if (x + kReads < N) vt[x % kReads] = in.value(x + kReads);
+#pragma unroll
+      for (int i = 0; i < kEach; i++) weight<KT>(w, p, kEach * x + i, scale, ref, part);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (rose) {
+      w.sum *= keep;
+#pragma unroll
+      for (int t = 0; t < DT; t++) w.o[t] *= keep;
+    }
+    w.sum += part[0] + part[1];
+#pragma unroll
+    for (int i = 0; i < 2 * KT; i++) w.p[i] = p[i];
   }
 
   // A tile's blocks [lo, hi): its result, or a partial one into `slot`.
@@ -384,7 +454,7 @@ struct Tiled {
     const int from = a.mask || !any ? ctx : ctx + first_row / a.G + 1;
     const int until = !any ? 0 : a.mask ? rq.len : ctx + (min(first_row + 31, rows - 1)) / a.G + 1;
     const int end = min(hi * KB, rq.len);
-    const int half = PAIRED ? 32 * KT * (wave & 1) : 0, late_wave = wave / (NW / 2);
+    const int half = PAIRED ? 32 * KT * (wave & 1) : 0, late_wave = kPhases && wave >= NW / 2;
     lds_char *buf = (lds_char *)L.buf, *ring = buf + kBuffers * kBuffer;
     int cur = 0, raw = 0;  // the turn's buffer, the ring's place that is fetched into
     if (threadIdx.x == 0) L.odd = 0;
@@ -418,6 +488,10 @@ struct Tiled {
         change_over<kInFlight>();
         begin(rows, now, next);
         rows = rows_after(L, rows, j + 1 + kAhead, lane, wave);
+        if constexpr (!kPhases) {
+          if (any) both<KT>(w, now, scale, lane);
+          continue;
+        }
         if (any) {
           if constexpr (late) weights<KT>(w, scale);
           else products<KT>(w, now, true, true, lane);
@@ -451,7 +525,7 @@ struct Tiled {
         }
         auto use = [&](int j) { return j >= lo && j < hi && j * KB + half < until; };
         for (int phase = 0; phase < 2; phase++) {
-          if (phase) change_over<63>();
+          if (phase && kPhases) change_over<63>();
           const int of = late && !phase ? j - 1 : j;  // whose arithmetic
           if (phase == late) products<KT>(w, now, use(j - 1), use(j), l);
           else if (use(of)) {
@@ -462,7 +536,7 @@ struct Tiled {
         }
       }
     };
-    if (late_wave) turns(std::true_type{});
+    if (late_wave) turns(std::integral_constant<bool, kPhases>{});
     else turns(std::false_type{});
     const bool odd = L.odd != 0;
     change_over<0>();  // LDS is free
@@ -522,10 +596,10 @@ struct Tiled {
 };
 
 template <bool BF, bool F8, int D>
-__global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kAttnThreads<D>, kAttnWaves<D> / 4) void attn_tile_kernel(AttnArgs a) {
   using S = Tiled<BF, F8, D>;
   __shared__ typename S::Lds L;
-  walk<S::RT, S::KB, kPairedRows<D>, D, kAttnThreads>(a, [&](const Tile &tile, int lo, int hi, int slot) {
+  walk<S::RT, S::KB, kPairedRows<D>, D, kAttnThreads<D>>(a, [&](const Tile &tile, int lo, int hi, int slot) {
     if constexpr (kPairedRows<D> > 0) {
       if (tile.rows <= kPairedRows<D>) return S::template segment<true>(a, L, tile, lo, hi, slot, gridDim.x);
     }

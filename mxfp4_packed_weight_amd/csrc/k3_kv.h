@@ -46,7 +46,7 @@ struct AttnArgs {
   uint32_t page_magic;  // a place p < 2^31 is in block umulhi(2p, page_magic) >> page_shift
   int page_shift;
 };
-int attn_tile_rows(int T, int G, int R);
+int attn_tile_rows(int T, int G, int R, int D);
 int attn_workgroups(int tile_rows);
 size_t attn_workspace_bytes(int T, int Hq, int n_heads, int D);
 hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t s);

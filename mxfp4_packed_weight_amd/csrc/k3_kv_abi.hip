@@ -17,21 +17,21 @@ hipError_t launch_attn_f16_e4m3(const AttnArgs &a, hipStream_t s);
 
 // Rows per tile: up to 32 rows of an average request go to the streaming
 // kernel, two workgroups to a CU; more to the tiled kernel, one to a CU.
-int attn_tile_rows(int T, int G, int R) {
+int attn_tile_rows(int T, int G, int R, int D) {
   const long long rows = ((long long)T * G + R - 1) / R;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 256;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : D == 256 ? 128 : 256;
 }
 
 int attn_workgroups(int tile_rows) {
   const int cus = std::min(num_cus(), kMaxWorkgroups / 2);
-  return tile_rows == 256 ? cus : 2 * cus;
+  return tile_rows > 32 ? cus : 2 * cus;
 }
 
 static int attn_part_rows(int tile_rows, int T, int G) { return (int)std::min((long long)tile_rows, (long long)T * G); }
 
 size_t attn_workspace_bytes(int T, int Hq, int n_heads, int D) {
   // R is not known here, and more requests only make the tiles smaller
-  const int G = Hq / n_heads, rows = attn_tile_rows(T, G, 1);
+  const int G = Hq / n_heads, rows = attn_tile_rows(T, G, 1, D);
   return (size_t)2 * attn_workgroups(rows) * attn_part_rows(rows, T, G) * (D + 2) * sizeof(float) +
          kMaxWorkgroups * sizeof(JoinJob);
 }
@@ -300,7 +300,7 @@ k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T, i
   a.blocks = blocks;
   a.R = R;
   a.words = words;
-  a.part_rows = attn_part_rows(attn_tile_rows(T, a.G, R), T, a.G);
+  a.part_rows = attn_part_rows(attn_tile_rows(T, a.G, R, D), T, a.G);
   // p / P = (p * m) >> (31 + s) for p < 2^31: s = ceil(log2 P), m the next
   // integer above 2^(31 + s) / P (m < 2^32, and m P - 2^(31 + s) <= 2^s)
   int shift = 0;
