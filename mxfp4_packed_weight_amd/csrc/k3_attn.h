@@ -241,8 +241,12 @@ __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
       job.row0 = tile.row0;
       job.rows = tile.rows;
       job.tail_slot = slot;
-      job.last = b;
-      while (job.last + 1 < B && line.begin(job.last + 1) < tile.after) job.last++;
+      int over = B;  // the first workgroup after it
+      for (job.last = b; over - job.last > 1;) {
+        const int mid = (job.last + over) >> 1;
+        if (line.begin(mid) < tile.after) job.last = mid;
+        else over = mid;
+      }
     }
     if (lo < hi) segment(tile, lo, hi, slot);
     u = tile.after;
