@@ -31,13 +31,13 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-// A block for a tile of up to half the waves' rows takes 10 / 16 of the time
-// of a full one.
-constexpr int kHalfCost = 10;
-// A tile's fixed cost, in blocks: its tables, queries and first blocks come
-// one after the other (about 10 us), and its results go out.
+// A block for a tile of up to half the waves' rows takes 11 / 16 of the time
+// of a full one, and what a tile takes apart from its blocks is that of so
+// many places: its tables, queries and first blocks come one after the other
+// (14 us, at 1.8 us for 64 places of a head of 128).
+constexpr int kHalfCost = 11;
 template <int RT>
-constexpr int kFixedBlocks = RT < 128 ? 1 : 6;
+constexpr int kFixedPlaces = RT < 128 ? 128 : 512;
 constexpr int kMaxWorkgroups = 1024;  // of a launch: at most two to a CU
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The running maximum is raised only by more than this (in powers of two):
@@ -64,28 +64,30 @@ __device__ __forceinline__ Request request_of(const AttnArgs &a, int r) {
   return q;
 }
 
-// The cost of a request's tiles, in sixteenths of a place: the first tile's,
-// what each next one has more, and the last one's, which counts for less if it
-// is of up to HALF rows. T * Hq <= 2^30 rows and 2^30 places keep all sums
-// below 2^61.
-template <int RT, int KB, int HALF>
+// The cost of a request's tiles, in sixteenths of a place: what each has
+// fixed, the first tile's places, what each next one has more. The last one's
+// places count for less if it is of up to HALF rows. T * Hq <= 2^30 rows and
+// 2^30 places keep all sums below 2^61.
+template <int RT, int HALF>
 struct Cost {
   int tiles, last_rows;
   long long base, slope, all;
-  static constexpr long long kFixed = 16 * KB * kFixedBlocks<RT>;  // queries in, results out
+  static constexpr long long kFixed = 16 * kFixedPlaces<RT>;
   __device__ __forceinline__ Cost(const AttnArgs &a, const Request &q) {
     const long long rows = (long long)q.n * a.G;
     tiles = (int)((rows + RT - 1) / RT);
     last_rows = (int)(rows - (long long)(tiles - 1) * RT);
     const bool causal = !a.mask && q.len >= q.n;
     slope = causal ? 16 * RT / a.G : 0;
-    base = kFixed + 16ll * (causal ? q.len - q.n : q.len) + slope;
+    base = 16ll * (causal ? q.len - q.n : q.len) + slope;
     all = tiles ? of_first(tiles - 1) + of(tiles - 1) : 0;
   }
-  // a tile's cost per 16 of `base`; the first x tiles of a key head; tile x
+  // a place's cost; the first x tiles of a key head; tile x
   __device__ __forceinline__ int weight(int x) const { return x == tiles - 1 && last_rows <= HALF ? kHalfCost : 16; }
-  __device__ __forceinline__ long long of_first(long long x) const { return x * base + slope * (x * (x - 1) / 2); }
-  __device__ __forceinline__ long long of(int x) const { return (base + slope * x) * weight(x) / 16; }
+  __device__ __forceinline__ long long of_first(long long x) const {
+    return x * (kFixed + base) + slope * (x * (x - 1) / 2);
+  }
+  __device__ __forceinline__ long long of(int x) const { return kFixed + (base + slope * x) * weight(x) / 16; }
   __device__ __forceinline__ long long of_request(const AttnArgs &a) const { return all * a.c.n_heads; }
 };
 
@@ -99,11 +101,11 @@ struct Line {
 template <int THREADS>
 __device__ __forceinline__ int run_of(int R) { return (R + THREADS - 1) / THREADS; }
 
-template <int RT, int KB, int HALF, int THREADS>
+template <int RT, int HALF, int THREADS>
 __device__ __forceinline__ void line_of_tiles(const AttnArgs &a, Line<THREADS> &L) {
   const int tid = threadIdx.x, lane = tid & 63, per = run_of<THREADS>(a.R);
   long long own = 0;
-  for (int r = tid * per; r < min(a.R, tid * per + per); r++) own += Cost<RT, KB, HALF>(a, request_of(a, r)).of_request(a);
+  for (int r = tid * per; r < min(a.R, tid * per + per); r++) own += Cost<RT, HALF>(a, request_of(a, r)).of_request(a);
   long long incl = own;
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) {
@@ -128,11 +130,26 @@ __device__ __forceinline__ long long in_all_lanes(long long x) {
 // A tile in the line.
 struct Tile {
   Request q;
-  int r, h, row0, rows;
+  int r, h, x;             // its request, key head, number
+  int row0, rows;
   int places, blocks;      // that its rows may see: the first `places`, in `blocks` blocks
   int weight;              // Cost::weight
   long long first, after;  // its stretch of the line
+  int tiles;               // of its key head
 };
+// The rest of a tile from q, r, h, x and first.
+template <int RT, int KB, int HALF>
+__device__ __forceinline__ void fill_tile(const AttnArgs &a, Tile &t, const Cost<RT, HALF> &cost) {
+  t.tiles = cost.tiles;
+  t.row0 = t.x * RT;
+  t.rows = t.x == cost.tiles - 1 ? cost.last_rows : RT;
+  t.weight = cost.weight(t.x);
+  t.after = t.first + cost.of(t.x);
+  t.places = t.q.len;
+  if (!a.mask) t.places = min(t.q.len, max(0, t.q.len - t.q.n + (t.row0 + t.rows - 1) / a.G + 1));
+  t.blocks = t.places > 0 ? (t.places - 1) / KB + 1 : 1;
+}
+// The tile that place u of the line is in.
 template <int RT, int KB, int HALF, int THREADS>
 __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &L, long long u) {
   Tile t;
@@ -148,30 +165,38 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &
   t.r = run * per;
   t.q = request_of(a, t.r);
   for (; t.r + 1 < min(a.R, run * per + per); t.r++) {
-    const long long all = Cost<RT, KB, HALF>(a, t.q).of_request(a);
+    const long long all = Cost<RT, HALF>(a, t.q).of_request(a);
     if (before + all > u) break;
     before += all;
     t.q = request_of(a, t.r + 1);
   }
-  const Cost<RT, KB, HALF> cost(a, t.q);
-  const long long x = u - before;
-  t.h = (int)(x / cost.all);
-  const long long in_head = x - t.h * cost.all;
+  const Cost<RT, HALF> cost(a, t.q);
+  t.h = (int)((u - before) / cost.all);
+  const long long head = before + t.h * cost.all;
   int lo = 0, hi = cost.tiles - 1;  // the last tile that begins at or before it
   while (lo < hi) {
     const int mid = lo + ((hi - lo + 1) >> 1);
-    if (cost.of_first(mid) <= in_head) lo = mid;
+    if (head + cost.of_first(mid) <= u) lo = mid;
     else hi = mid - 1;
   }
-  t.row0 = lo * RT;
-  t.rows = lo == cost.tiles - 1 ? cost.last_rows : RT;
-  t.weight = cost.weight(lo);
-  t.first = before + t.h * cost.all + cost.of_first(lo);
-  t.after = t.first + cost.of(lo);
-  t.places = t.q.len;
-  if (!a.mask) t.places = min(t.q.len, max(0, t.q.len - t.q.n + (t.row0 + t.rows - 1) / a.G + 1));
-  t.blocks = t.places > 0 ? (t.places - 1) / KB + 1 : 1;
+  t.x = lo;
+  t.first = head + cost.of_first(lo);
+  fill_tile<RT, KB, HALF>(a, t, cost);
   return t;
+}
+// The next tile (there is one).
+template <int RT, int KB, int HALF>
+__device__ __forceinline__ void next_tile(const AttnArgs &a, Tile &t) {
+  t.first = t.after;
+  if (++t.x == t.tiles) {
+    t.x = 0;
+    if (++t.h == a.c.n_heads) {
+      t.h = 0;
+      do t.q = request_of(a, ++t.r);
+      while (t.q.n == 0 && t.r + 1 < a.R);
+    }
+  }
+  fill_tile<RT, KB, HALF>(a, t, Cost<RT, HALF>(a, t.q));
 }
 
 // The tile's first block that is done after place u of the line.
@@ -180,7 +205,7 @@ __device__ __forceinline__ int block_from(const Tile &t, long long u) {
   if (u <= t.first) return 0;
   if (u >= t.after) return t.blocks;
   const int each = KB * t.weight;  // a block's cost
-  const long long y = max(u - t.first - each * kFixedBlocks<RT>, 0ll);
+  const long long y = max(u - t.first - 16 * kFixedPlaces<RT>, 0ll);
   return (int)min((y + each - 1) / each, (long long)t.blocks);
 }
 
@@ -225,13 +250,15 @@ __device__ __forceinline__ JoinJob *join_jobs(const AttnArgs &a, int B) {
 template <int RT, int KB, int HALF, int D, int THREADS, class Segment>
 __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
   __shared__ Line<THREADS> L;
-  line_of_tiles<RT, KB, HALF, THREADS>(a, L);
+  line_of_tiles<RT, HALF, THREADS>(a, L);
   const int B = gridDim.x, b = place_in_line(blockIdx.x, B);
   const Stretches line(in_all_lanes(L.pre[THREADS]), B);
   const long long begin = line.begin(b), end = line.begin(b + 1);
   JoinJob job = {0, 0, 0, 0, -1, -1, -1, 0};
+  Tile tile;
   for (long long u = begin; u < end;) {
-    const Tile tile = tile_at<RT, KB, HALF>(a, L, u);
+    if (u == begin) tile = tile_at<RT, KB, HALF>(a, L, u);
+    else next_tile<RT, KB, HALF>(a, tile);
     const int lo = block_from<RT, KB>(tile, u), hi = block_from<RT, KB>(tile, end);
     const int slot = lo == hi || (lo == 0 && hi == tile.blocks) ? -1 : lo ? 2 * b : 2 * b + 1;
     if (u > tile.first) job.head_slot = slot;

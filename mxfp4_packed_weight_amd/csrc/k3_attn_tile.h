@@ -438,7 +438,7 @@ struct Tiled {
     const uint16_t *q = a.q + (int64_t)(rq.t0 + node) * a.q_stride + hq * D + 8 * h;
 #pragma unroll
     for (int s = 0; s < NS; s++)
-      w.q[s] = on && a.scale != 0.f ? *(const u32x4 *)(q + 16 * s) ^ round : u32x4{0, 0, 0, 0};
+      w.q[s] = on && a.scale != 0.f ? *(const u32x4 *)(q + 16 * s) : u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int t = 0; t < DT; t++) w.o[t] = f32x16{};
     w.ref = -INFINITY;
@@ -459,6 +459,8 @@ struct Tiled {
     int cur = 0, raw = 0;  // the turn's buffer, the ring's place that is fetched into
     if (threadIdx.x == 0) L.odd = 0;
     uint64_t holes = list(a, L, table, lo & -(kListed / 2), end, 0);  // blocks with places that are not there
+#pragma unroll
+    for (int s = 0; s < NS; s++) w.q[s] ^= round;  // (only here are they waited for)
     // Begins turn j: fetches `rows` for a later one, and says where this one's
     // keys and values are, and the next one's.
     auto begin = [&](const Rows &rows, const lds_char *&now, lds_char *&next) {
