@@ -4,7 +4,7 @@
 // several rows or parts go out together. Tiles in few parts: four values of
 // four rows per thread, part by part. Tiles in many (long rows of few
 // requests): a wave per row, as many parts side by side as lanes allow and
-// eight of those in flight.
+// up to sixteen of those in flight.
 #pragma once
 
 #include <algorithm>
@@ -18,11 +18,30 @@ constexpr int kJoinWaves = 4, kFewParts = 6;
 
 template <bool BF, int D>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, int B) {
-  __shared__ int lists[kJoinWaves][kMaxWorkgroups + 1];
-  const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ int lists[kJoinWaves][kMaxWorkgroups + 1], jobs_of[kMaxWorkgroups], found[kJoinWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const JoinJob *jobs = join_jobs<D>(a, B);
+  // the jobs that there are, shared out to the workgroups
+  int count = 0;
+  for (int x0 = 0; x0 < B; x0 += 64 * kJoinWaves) {
+    const int x = x0 + threadIdx.x;
+    const bool there = x < B && jobs[x].rows > 0;
+    const uint64_t all = __ballot(there);
+    if (lane == 0) found[wave] = __popcll(all);
+    __syncthreads();
+    int at = count + __popcll(all & ((1ull << lane) - 1));
+    for (int w = 0; w < kJoinWaves; w++) {
+      if (w < wave) at += found[w];
+      count += found[w];
+    }
+    if (there) jobs_of[at] = x;
+    __syncthreads();
+  }
+  const int share = blockIdx.x % max(count, 1), chunk = blockIdx.x / max(count, 1);
+  const int chunks = ((int)gridDim.x - share + count - 1) / max(count, 1);
+  if (count == 0) return;
+  const int b = __builtin_amdgcn_readfirstlane(jobs_of[share]);
   const JoinJob job = jobs[b];
-  if (job.rows == 0) return;
   int *slots = lists[wave], n = 0;
   for (int x0 = b; x0 <= job.last; x0 += 64) {
     const int x = x0 + lane;
@@ -46,7 +65,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
   };
   if (n <= kFewParts) {
     constexpr int ROWS = 4, PASS = 64 * kJoinWaves / LPR;  // rows of a thread, rows side by side
-    for (int r0 = blockIdx.y * ROWS * PASS; r0 < job.rows; r0 += gridDim.y * ROWS * PASS) {
+    for (int r0 = chunk * ROWS * PASS; r0 < job.rows; r0 += chunks * ROWS * PASS) {
       float ref[ROWS], sum[ROWS];
       f32x4 o[ROWS];
 #pragma unroll 2
@@ -80,7 +99,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
     return;
   }
   const int sub = lane / LPR;
-  for (int r = blockIdx.y * kJoinWaves + wave; r < job.rows; r += gridDim.y * kJoinWaves) {
+  for (int r = chunk * kJoinWaves + wave; r < job.rows; r += chunks * kJoinWaves) {
     float ref = -INFINITY, sum = 0.f;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     auto join = [&](auto ahead, int x0) {
@@ -111,6 +130,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
         }
     };
     int x0 = 0;
+    for (; x0 + 8 * SIDE < n; x0 += 16 * SIDE) join(std::integral_constant<int, 16>{}, x0);
     for (; x0 + 2 * SIDE < n; x0 += 8 * SIDE) join(std::integral_constant<int, 8>{}, x0);
     for (; x0 < n; x0 += SIDE) join(std::integral_constant<int, 1>{}, x0);
 #pragma unroll
@@ -126,14 +146,11 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
   }
 }
 
-// Workgroups to a tile: enough for its rows in few parts, and for the card
-// where there are few tiles.
-template <int D>
-inline int join_height(const AttnArgs &a, int B) {
-  const long long tiles = (long long)a.R * (((long long)a.T * a.G + a.R * 256ll - 1) / (a.R * 256ll)) * a.c.n_heads;
-  const int few = (a.part_rows * D / 16 + 64 * kJoinWaves - 1) / (64 * kJoinWaves);
-  const int most = (a.part_rows + kJoinWaves - 1) / kJoinWaves;
-  return std::min(most, std::max(few, (int)(2048 / std::min<long long>(tiles, B))));
+// Workgroups of the launch: four rows each of the tiles that may be split, up
+// to eight for each CU, and never fewer than those tiles.
+inline int join_workgroups(const AttnArgs &a, int B) {
+  const long long tiles = std::min<long long>(B, (a.R + (long long)a.T * a.G / a.part_rows) * a.c.n_heads);
+  return (int)std::min<long long>(2 * kMaxWorkgroups, tiles * ((a.part_rows + kJoinWaves - 1) / kJoinWaves));
 }
 
 }  // namespace k3

@@ -24,7 +24,7 @@ int attn_tile_rows(int T, int G, int R, int D) {
 
 int attn_workgroups(int tile_rows) {
   const int cus = std::min(num_cus(), kMaxWorkgroups / 2);
-  return tile_rows > 32 ? cus : 2 * cus;
+  return tile_rows == 16 ? 2 * cus : cus;
 }
 
 static int attn_part_rows(int tile_rows, int T, int G) { return (int)std::min((long long)tile_rows, (long long)T * G); }
