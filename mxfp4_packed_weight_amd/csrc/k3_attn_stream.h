@@ -14,8 +14,7 @@
 //                 16 (j / 4) + 4 g + j % 4, which is what the lane's scores
 //                 are. V is read in rows (16 lanes side by side cover a row,
 //                 D / 16 values each) and turned within the lane by byte
-//                 permutes; product e takes value e of each lane's, so its
-//                 row m is value m * D / 16 + e.
+//                 permutes; product e takes value e of each lane's.
 // Maximum and sum are the row's own lanes', but for two lane swaps. Only the
 // maximum's large rises rescale the output (kSlack).
 //
@@ -77,6 +76,13 @@ struct Stream {
     return (uint32_t)__ballot(there);
   }
 
+  // Keys and values are read once, so they pass the caches by (not kept there
+  // for later: 5.25 -> 5.95 TB/s, 64 requests of up to 8191 places).
+  template <class T>
+  static __device__ __forceinline__ T read_once(const char *p) {
+    return __builtin_nontemporal_load((const T *)p);
+  }
+
   static __device__ __forceinline__ void load_k(Wave &w, const char *k, const int64_t *offset, int c, int g) {
 #pragma unroll
     for (int u = 0; u < 2; u++) {
@@ -84,7 +90,7 @@ struct Stream {
       if (F8) {
 #pragma unroll
         for (int s = 0; s < NS; s += 2) {
-          const u32x4 x = *(const u32x4 *)(p + d_of(s, g));
+          const u32x4 x = read_once<u32x4>(p + d_of(s, g));
           w.k[u][s][0] = x[0];
           w.k[u][s][1] = x[1];
           w.k[u][s + 1][0] = x[2];
@@ -93,7 +99,7 @@ struct Stream {
       } else {
 #pragma unroll
         for (int s = 0; s < NS; s++) {
-          const u32x4 x = *(const u32x4 *)(p + 2 * d_of(s, g));
+          const u32x4 x = read_once<u32x4>(p + 2 * d_of(s, g));
 #pragma unroll
           for (int i = 0; i < KW; i++) w.k[u][s][i] = x[i];
         }
@@ -101,20 +107,25 @@ struct Stream {
     }
   }
 
+  // Value e of those that lane c has: runs of 16 bytes, so that 16 lanes' runs
+  // lie side by side.
+  static constexpr int kRun = DPL < 16 / ES ? DPL : 16 / ES;
+  static __device__ __forceinline__ int value_of(int c, int e) { return 16 * kRun * (e / kRun) + kRun * c + e % kRun; }
+
   static __device__ __forceinline__ void load_v(Wave &w, const char *v, const int64_t *offset, int c, int g) {
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      const char *p = v + offset[16 * (j / 4) + 4 * g + j % 4] + c * (VW * 4);
+      const char *p = v + offset[16 * (j / 4) + 4 * g + j % 4];
       if constexpr (VW == 1) {
-        w.v[j][0] = *(const uint32_t *)p;
+        w.v[j][0] = read_once<uint32_t>(p + c * 4);
       } else if constexpr (VW == 2) {
-        const u32x2 x = *(const u32x2 *)p;
+        const u32x2 x = read_once<u32x2>(p + c * 8);
         w.v[j][0] = x[0];
         w.v[j][1] = x[1];
       } else {
 #pragma unroll
         for (int i = 0; i < VW; i += 4) {
-          const u32x4 x = *(const u32x4 *)(p + 4 * i);
+          const u32x4 x = read_once<u32x4>(p + 64 * i + c * 16);
 #pragma unroll
           for (int e = 0; e < 4; e++) w.v[j][i + e] = x[e];
         }
@@ -190,7 +201,7 @@ struct Stream {
       for (int r = 0; r < 4; r++)
 #pragma unroll
         for (int e = 0; e < DPL; e++) {
-          const int d = DPL * (4 * g + r) + e;
+          const int d = value_of(4 * g + r, e);
           float x;
           if (F8) {
             const uint32_t b = ((const uint8_t *)row)[d];
@@ -368,7 +379,7 @@ struct Stream {
         for (int e = 0; e < DPL; e += 4) {
           const f32x4 x = {w.o[t][e][r] * keep, w.o[t][e + 1][r] * keep, w.o[t][e + 2][r] * keep,
                            w.o[t][e + 3][r] * keep};
-          *(f32x4 *)(mine + DPL * (4 * g + r) + e) = x;
+          *(f32x4 *)(mine + value_of(4 * g + r, e)) = x;
         }
       __syncthreads();
       for (int x = tid; x < 16 * (D / 4); x += kStreamThreads) {
