@@ -17,6 +17,7 @@ import numpy as np
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libk3moe.so")
 _lib = None
+_functions = {}  # those called so far
 
 K3_OK, K3_ERR_ARG, K3_ERR_CONFIG, K3_ERR_MEMORY, K3_ERR_DEVICE = 0, 1, 2, 3, 4
 K3_MAX_EXPERTS, K3_MAX_TOPK, K3_MAX_SHARED = 4096, 64, 8
@@ -159,7 +160,10 @@ def last_error():
 
 
 def _call(name, *args):
-    rc = getattr(lib(), name)(*args)
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(lib(), name)
+    rc = f(*args)
     if rc != K3_OK:
         raise K3Error(name, rc, last_error())
     return rc
@@ -178,10 +182,20 @@ def _hp(a):
     return None if a is None else ctypes.c_void_p(a.ctypes.data)
 
 
+_current = None
+
+
 def _stream(stream=None):
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The handle of a stream, or of the current device's current one (asked
+    for without the stream object: 0.3 us instead of 3)."""
+    global _current
+    if stream is not None:
+        return stream.cuda_stream
+    if _current is None:
+        import torch
+        torch.cuda.init()
+        _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _current[0](_current[1]())
 
 
 # ---- layout ---------------------------------------------------------------
@@ -519,25 +533,32 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_kv_codes = {}
+
+
 def _kv_dtype(t):
-    import torch
-    codes = {torch.bfloat16: K3_BF16, torch.float16: K3_F16, torch.float8_e4m3fn: K3_E4M3}
-    if t.dtype not in codes:
+    if not _kv_codes:
+        import torch
+        _kv_codes.update({torch.bfloat16: K3_BF16, torch.float16: K3_F16,
+                          torch.float8_e4m3fn: K3_E4M3})
+    code = _kv_codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"bfloat16, float16 or float8_e4m3fn, not {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
 def _heads(name, t, dtype, D):
     """Token stride of rows [T, heads, D] or [T, heads * D] with dense heads."""
     if _kv_dtype(t) != dtype:
         raise TypeError(f"{name} is {t.dtype}, not the type of the call's other rows")
-    dense = t.dim() in (2, 3) and t.stride(-1) == 1
-    if dense and t.dim() == 3:
-        dense = t.shape[2] == D and (t.shape[1] == 1 or t.stride(1) == D)
+    shape, strides = t.shape, t.stride()
+    dense = len(shape) in (2, 3) and strides[-1] == 1
+    if dense and len(shape) == 3:
+        dense = shape[2] == D and (shape[1] == 1 or strides[1] == D)
     if not dense:
         raise ValueError(f"{name}: rows [T, heads, {D}] with dense heads, "
-                         f"not {tuple(t.shape)} with strides {t.stride()}")
-    return t.stride(0)
+                         f"not {tuple(shape)} with strides {strides}")
+    return strides[0]
 
 
 def k3_kv_cache_of(k, v, k_scale=None, v_scale=None):
