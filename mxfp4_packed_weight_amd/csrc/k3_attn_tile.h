@@ -97,11 +97,12 @@ struct Tiled {
     return D == 64 ? 2 * r : 2 * (2 * r ^ (r >> 1));
   }
 
-  // Byte offset of a place's row; -1 if it has no page.
-  static __device__ __forceinline__ int64_t place(const AttnArgs &a, const int32_t *table, int p, int end) {
-    if (p >= end) return -1;
-    const uint32_t b = __umulhi(2u * (uint32_t)p, a.page_magic) >> a.page_shift;
-    const int page = b < (uint32_t)a.blocks ? table[b] : -1;
+  static __device__ __forceinline__ uint32_t block_of(const AttnArgs &a, int p) {
+    return __umulhi(2u * (uint32_t)p, a.page_magic) >> a.page_shift;
+  }
+  // Byte offset of the row of place p, whose page (block b) is `page`; -1 if
+  // there is no such page.
+  static __device__ __forceinline__ int64_t row_of(const AttnArgs &a, int p, uint32_t b, int page) {
     if (page < 0 || page >= a.c.n_pages) return -1;
     return (page * a.c.page_stride + (int)((uint32_t)p - b * a.c.page_size) * a.c.slot_stride) * ES;
   }
@@ -110,10 +111,15 @@ struct Tiled {
   static __device__ __forceinline__ uint64_t list(const AttnArgs &a, Lds &L, const int32_t *table, int x, int end,
                                                   uint64_t holes) {
     const int at = x % kListed;
+    constexpr int N = kListed / 2 * KB / kThreads;
+    int page[N];  // (all loads at once: the table has at least one entry)
 #pragma unroll
-    for (int i = 0; i < kListed / 2 * KB / kThreads; i++) {
-      const int n = i * kThreads + threadIdx.x;
-      const int64_t row = place(a, table, x * KB + n, end);
+    for (int i = 0; i < N; i++)
+      page[i] = table[min(block_of(a, x * KB + i * kThreads + threadIdx.x), (uint32_t)a.blocks - 1)];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const int n = i * kThreads + threadIdx.x, p = x * KB + n;
+      const int64_t row = p < end ? row_of(a, p, block_of(a, p), page[i]) : -1;
       L.row[at * KB + n] = row < 0 ? 0 : row;
       const uint64_t there = __ballot(row >= 0);
       if (n % 32 == 0) L.present[at * (KB / 32) + n / 32] = (uint32_t)(there >> (n & 32));
@@ -134,7 +140,7 @@ struct Tiled {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to)), "v"(from)
-                 : "memory");
+                 : "m0", "memory");
   }
   // Where the rows are that a wave loads in a turn: keys of block x, values of
   // block x - 1 (the first turn has none: block `lo`, which is listed).
@@ -233,7 +239,8 @@ struct Tiled {
   static __device__ __forceinline__ void add_not_finite(const AttnArgs &a, f32x16 *o, const Request &rq, int node,
                                                         const char *v, const int32_t *table, int p, int end, int h) {
     for (; p < end; p++) {
-      const int64_t at = place(a, table, p, end);
+      const uint32_t b = block_of(a, p);
+      const int64_t at = row_of(a, p, b, table[b]);
       if (at < 0 || !(seen(a, rq, node, p, 1) & 1)) continue;
       const char *row = v + at;
 #pragma unroll
