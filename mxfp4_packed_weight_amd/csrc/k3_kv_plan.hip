@@ -4,7 +4,7 @@
 // Everything follows from three prefix sums over the requests (tokens, pages
 // taken, pages given back), so no workgroup waits for another: each redoes
 // the sums (a thousand requests are 12 KB of reads out of L2 and one scan)
-// and then does its own share of the requests' pages and of the tokens. The
+// and then does its own share of the requests' pages or of the tokens. The
 // reads and the updates in place do not meet: the ring's taken entries are
 // never among those written (count + given back <= n_pages is checked), and
 // a table entry is written only past held[r], where no one reads.
@@ -58,15 +58,19 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
   int head = a.ring_state[0];
   const int count = min(max(a.ring_state[1], 0), N);
   if (head < 0 || head >= N) head = 0;
-  const int t0 = blockIdx.x * kPlanThreads, t = t0 + tid;
+  const int token_groups = (a.T + kPlanThreads - 1) / kPlanThreads;
+  // the first workgroups take the pages, the others the tokens
+  const int page_groups = gridDim.x - token_groups;
+  const bool pages = (int)blockIdx.x < page_groups;
+  const int t0 = pages ? a.T : (blockIdx.x - page_groups) * kPlanThreads, t = t0 + tid;
   // parents of every node that shares a request with this workgroup's tokens
   if (a.parents && t0 < a.T)
     for (int i = tid; i < 3 * kNodes; i += kPlanThreads) {
       const int s = t0 - kNodes + i;
       L.parents[i] = s >= 0 && s < a.T ? a.parents[s] : -1;
     }
-  const int per = (a.R + gridDim.x - 1) / gridDim.x;  // requests whose pages are moved here
-  const int r_lo = blockIdx.x * per, r_hi = min(a.R, r_lo + per);
+  const int per = (a.R + page_groups - 1) / page_groups;  // requests whose pages are moved here
+  const int r_lo = min(a.R, (int)blockIdx.x * per), r_hi = pages ? min(a.R, r_lo + per) : r_lo;
   const bool tells = blockIdx.x == 0;
   if (tid == 0) L.taken = L.given = 0;
   uint32_t cu0 = 0, pops0 = 0, push0 = 0;
@@ -150,14 +154,11 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
       }
       const int i = t - (int)L.cu[lo];
       const long long p = (long long)L.ctx[lo] + i;
-      int slot = -1;
-      if (L.need[lo] >= 0) {
-        const int b = (int)p / P;
-        const int page = b < L.held[lo] ? a.table[(size_t)(c0 + lo) * a.blocks + b]
-                                        : a.ring[in_ring(head + L.pops[lo] + b - L.held[lo], N)];
-        if (page >= 0 && page < N) slot = page * P + ((int)p - b * P);
-      }
-      a.slots[t] = slot;
+      const int b = (int)p / P;
+      int page = -1;  // (not waited for before the tree's walk)
+      if (L.need[lo] >= 0)
+        page = b < L.held[lo] ? a.table[(size_t)(c0 + lo) * a.blocks + b]
+                              : a.ring[in_ring(head + L.pops[lo] + b - L.held[lo], N)];
       int depth = i;
       if (a.parents) {
         const int n_r = L.n[lo], base = tid + kNodes - i;  // node 0 in the window
@@ -187,6 +188,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
           }
         }
       }
+      a.slots[t] = page >= 0 && page < N ? page * P + ((int)p - b * P) : -1;
       a.positions[t] = (int)min(max((long long)L.ctx[lo] + depth, -2147483648ll), 2147483647ll);
     }
     cu0 = c_end;
@@ -211,7 +213,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
 }  // namespace
 
 hipError_t launch_kv_plan(const KvPlanArgs &a, hipStream_t s) {
-  const int grid = max(max((a.T + kPlanThreads - 1) / kPlanThreads, (a.R + kPlanWaves - 1) / kPlanWaves), 1);
+  const int grid = (a.T + kPlanThreads - 1) / kPlanThreads + (a.R + kPlanWaves - 1) / kPlanWaves;
   kv_plan_kernel<<<grid, kPlanThreads, 0, s>>>(a);
   return hipGetLastError();
 }
