@@ -4,7 +4,8 @@
 // several rows or parts go out together. Tiles in few parts: four values of
 // four rows per thread, part by part. Tiles in many (long rows of few
 // requests): a wave per row, as many parts side by side as lanes allow and
-// up to sixteen of those in flight.
+// up to sixteen of those in flight. One token over 4096 places: 5 us after the
+// main launch's 11; 32 trees of up to 64 nodes, 47 MB of parts: 16 us.
 #pragma once
 
 #include <algorithm>

@@ -32,7 +32,9 @@ template <bool BF, bool F8, int D>
 hipError_t launch_attn(const AttnArgs &a, hipStream_t s) {
   switch (attn_tile_rows(a.T, a.G, a.R, D)) {
     case 16: return launch_stream<BF, F8, D, 1>(a, s);
-    case 32: return launch_stream<BF, F8, D, 2>(a, s);
+    case 32:
+      if constexpr (D < 256) return launch_stream<BF, F8, D, 2>(a, s);
+      return hipErrorInvalidValue;
     default: return launch_tile<BF, F8, D>(a, s);
   }
 }

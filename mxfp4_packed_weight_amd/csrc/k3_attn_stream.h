@@ -20,6 +20,10 @@
 //
 // The rows' places come from the page table one run ahead, through a few
 // hundred bytes of LDS per wave.
+//
+// Measured: one token of each of 64 requests of up to 8191 places, 8 key heads
+// of 128 in bf16, 1.09 GB: 188 us, 5.7 TB/s (a copy on this card moves 5.0, a
+// plain read up to 7.0); in e4m3 115 us.
 #pragma once
 
 #include "k3_attn.h"

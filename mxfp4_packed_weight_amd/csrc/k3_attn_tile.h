@@ -23,7 +23,19 @@
 //                 transposing read, four places of one column to a lane.
 // A row of LDS is cut into 16-byte chunks whose places are permuted by the
 // row's number, so that the reads of 32 rows' same chunk (keys) and of four
-// rows' neighbouring chunks (values) spread over the banks.
+// rows' neighbouring chunks (values) spread over the banks (no conflicts
+// counted in 16-bit caches).
+//
+// Measured on 32 requests of 256 rows over 8192 places, 8 key heads of 128,
+// bf16: 306 us (898 TFLOP/s, 3.6 TB/s), 252 us (1090 TFLOP/s) where the pages
+// are few and stay in the caches; a large product of the library reaches 1227.
+// What made it: reads four products ahead and in program order (390 -> 354 us),
+// copies two turns ahead and no registers on the way (354 -> 337; three turns
+// are no faster), the two phases (337 -> 312), products before arithmetic at
+// issue (309 -> 305). Beside products the vector unit's own instructions run
+// at about half their rate, exponentials freely, so that a phase is bound by
+// both units together. Two waves to 32 rows: 250 -> 227 us at 128 rows.
+// Heads of 256, 128 rows: 650 TFLOP/s at 5.2 TB/s, 904 with few pages.
 #pragma once
 
 #include <type_traits>

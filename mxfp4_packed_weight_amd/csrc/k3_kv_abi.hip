@@ -15,13 +15,24 @@ hipError_t launch_attn_bf16_e4m3(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_f16(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_f16_e4m3(const AttnArgs &a, hipStream_t s);
 
-// Rows per tile: up to 32 rows of an average request go to the streaming
-// kernel, two workgroups to a CU; more to the tiled kernel, one to a CU.
+// Rows per tile: up to 32 rows of an average request (16 at a head of 256) go
+// to the streaming kernel, more to the tiled kernel. Streaming against tiled,
+// 32 requests of 8192 places, us:
+//   rows             16          32          48
+//   128, bf16     175 / 197   177 / 197   343 / 198
+//   128, e4m3     100 / 140   124 / 141   239 / 156
+//    64, bf16      95 / 104   103 / 104   197 / 107
+//   256, bf16     195 / 205   318 / 207   563 / 212
+// and 63 requests of one token with one of 512, 8 rows to a node: 381 / 224.
 int attn_tile_rows(int T, int G, int R, int D) {
   const long long rows = ((long long)T * G + R - 1) / R;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : D == 256 ? 128 : 256;
+  if (rows <= 16) return 16;
+  if (D == 256) return 128;
+  return rows <= 32 ? 32 : 256;
 }
 
+// Two workgroups of the streaming kernel's 16-row tiles fit on a CU, one of
+// the others.
 int attn_workgroups(int tile_rows) {
   const int cus = std::min(num_cus(), kMaxWorkgroups / 2);
   return tile_rows == 16 ? 2 * cus : cus;
