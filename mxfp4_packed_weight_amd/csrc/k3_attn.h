@@ -64,6 +64,14 @@ __device__ __forceinline__ Request request_of(const AttnArgs &a, int r) {
   return q;
 }
 
+// Row `row`'s node (its head in the group: row - node * G).
+__device__ __forceinline__ int node_of(const AttnArgs &a, int row) {
+  return (int)(__umulhi(2u * (uint32_t)row, a.group_magic) >> a.group_shift);
+}
+
+// (No divisions in what follows: a workgroup's way to its first block is a few
+// hundred instructions that it runs once, and each 64-bit division is a
+// hundred more to fetch.)
 // The cost of a request's tiles, in sixteenths of a place: what each has
 // fixed, the first tile's places, what each next one has more. The last one's
 // places count for less if it is of up to HALF rows. T * Hq <= 2^30 rows and
@@ -78,7 +86,7 @@ struct Cost {
     tiles = (int)((rows + RT - 1) / RT);
     last_rows = (int)(rows - (long long)(tiles - 1) * RT);
     const bool causal = !a.mask && q.len >= q.n;
-    slope = causal ? 16 * RT / a.G : 0;
+    slope = causal ? a.slope : 0;
     base = 16ll * (causal ? q.len - q.n : q.len) + slope;
     all = tiles ? of_first(tiles - 1) + of(tiles - 1) : 0;
   }
@@ -87,7 +95,7 @@ struct Cost {
   __device__ __forceinline__ long long of_first(long long x) const {
     return x * (kFixed + base) + slope * (x * (x - 1) / 2);
   }
-  __device__ __forceinline__ long long of(int x) const { return kFixed + (base + slope * x) * weight(x) / 16; }
+  __device__ __forceinline__ long long of(int x) const { return kFixed + ((base + slope * x) * weight(x) >> 4); }
   __device__ __forceinline__ long long of_request(const AttnArgs &a) const { return all * a.c.n_heads; }
 };
 
@@ -146,7 +154,7 @@ __device__ __forceinline__ void fill_tile(const AttnArgs &a, Tile &t, const Cost
   t.weight = cost.weight(t.x);
   t.after = t.first + cost.of(t.x);
   t.places = t.q.len;
-  if (!a.mask) t.places = min(t.q.len, max(0, t.q.len - t.q.n + (t.row0 + t.rows - 1) / a.G + 1));
+  if (!a.mask) t.places = min(t.q.len, max(0, t.q.len - t.q.n + node_of(a, t.row0 + t.rows - 1) + 1));
   t.blocks = t.places > 0 ? (t.places - 1) / KB + 1 : 1;
 }
 // The tile that place u of the line is in.
@@ -171,7 +179,11 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &
     t.q = request_of(a, t.r + 1);
   }
   const Cost<RT, HALF> cost(a, t.q);
-  t.h = (int)((u - before) / cost.all);
+  // (the product is off by less than 1: n_heads <= 2^10)
+  t.h = (int)((double)(u - before) * __builtin_amdgcn_rcp((double)cost.all));
+  t.h = min(max(t.h, 0), a.c.n_heads - 1);
+  if (t.h * cost.all > u - before) t.h--;
+  else if ((t.h + 1) * cost.all <= u - before) t.h++;
   const long long head = before + t.h * cost.all;
   int lo = 0, hi = cost.tiles - 1;  // the last tile that begins at or before it
   while (lo < hi) {
@@ -199,22 +211,25 @@ __device__ __forceinline__ void next_tile(const AttnArgs &a, Tile &t) {
   fill_tile<RT, KB, HALF>(a, t, Cost<RT, HALF>(a, t.q));
 }
 
-// The tile's first block that is done after place u of the line.
+// The tile's first block that is done after place u of the line (any rising
+// function would do).
 template <int RT, int KB>
 __device__ __forceinline__ int block_from(const Tile &t, long long u) {
   if (u <= t.first) return 0;
   if (u >= t.after) return t.blocks;
-  const int each = KB * t.weight;  // a block's cost
-  const long long y = max(u - t.first - 16 * kFixedPlaces<RT>, 0ll);
-  return (int)min((y + each - 1) / each, (long long)t.blocks);
+  static_assert(kHalfCost == 11 && (KB & (KB - 1)) == 0, "");
+  long long y = max(u - t.first - 16 * kFixedPlaces<RT>, 0ll);
+  if (t.weight != 16) y = y * 93 >> 6;  // 16 / 11
+  return (int)min((y + 16 * KB - 1) / (16 * KB), (long long)t.blocks);
 }
 
-// Where workgroup b's stretch of the line begins.
+// Where workgroup b's stretch of the line begins: equal ones, the last a
+// little shorter.
 struct Stretches {
-  long long each;
-  uint32_t rest, B;
-  __device__ __forceinline__ Stretches(long long cost, int B) : each(cost / B), rest((uint32_t)(cost % B)), B(B) {}
-  __device__ __forceinline__ long long begin(int b) const { return each * b + rest * (uint32_t)b / B; }
+  long long cost, each;
+  __device__ __forceinline__ Stretches(const AttnArgs &a, long long cost)
+      : cost(cost), each((long long)((double)cost * a.inv_groups) + (cost >> 50) + 1) {}
+  __device__ __forceinline__ long long begin(int b) const { return min(cost, each * b); }
 };
 // Neighbours in the line read the same keys: they go to one die (workgroups
 // go to the eight dies in turn, and each has an L2 of its own).
@@ -252,7 +267,7 @@ __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
   __shared__ Line<THREADS> L;
   line_of_tiles<RT, HALF, THREADS>(a, L);
   const int B = gridDim.x, b = place_in_line(blockIdx.x, B);
-  const Stretches line(in_all_lanes(L.pre[THREADS]), B);
+  const Stretches line(a, in_all_lanes(L.pre[THREADS]));
   const long long begin = line.begin(b), end = line.begin(b + 1);
   JoinJob job = {0, 0, 0, 0, -1, -1, -1, 0};
   Tile tile;

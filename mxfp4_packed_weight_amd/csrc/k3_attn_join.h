@@ -57,7 +57,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
   const int d = lane % LPR * 4;
   auto weight = [&](float m, float top) { return m == top ? 1.f : exp2_hw(m - top); };
   auto store = [&](int r, float ref, float sum, f32x4 o) {
-    const int row = job.row0 + r, i = row / a.G, hq = job.h * a.G + row - i * a.G;
+    const int row = job.row0 + r, i = node_of(a, row), hq = job.h * a.G + row - i * a.G;
     const size_t tok = job.t0 + i;
     const float f = sum == 0.f ? 0.f : (a.c.v_scale ? a.c.v_scale[job.h] : 1.f) / sum;
     *(u32x2 *)(a.out + tok * a.out_stride + hq * D + d) =

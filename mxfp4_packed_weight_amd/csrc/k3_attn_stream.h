@@ -318,7 +318,7 @@ struct Stream {
     for (int t = 0; t < QT; t++) {
       const int row = tile.row0 + 16 * t + c;
       const bool on = row < rows;
-      const int i = on ? row / a.G : 0, hq = tile.h * a.G + (on ? row - i * a.G : 0);
+      const int i = on ? node_of(a, row) : 0, hq = tile.h * a.G + (on ? row - i * a.G : 0);
       node[t] = i;
       const uint16_t *q = a.q + (rq.t0 + i) * a.q_stride + hq * D;
 #pragma unroll
@@ -399,7 +399,7 @@ struct Stream {
           o += *(const f32x4 *)(L.o[i] + rr * kPad + d);
         }
         if (slot < 0) {
-          const int i = row / a.G, hq = tile.h * a.G + row - i * a.G;
+          const int i = node_of(a, row), hq = tile.h * a.G + row - i * a.G;
           const size_t tok = tile.q.t0 + i;
           const float f = sum == 0.f ? 0.f : v_scale / sum;
           u32x2 y = {pack2<BF>(o[0] * f, o[1] * f), pack2<BF>(o[2] * f, o[3] * f)};

@@ -448,7 +448,7 @@ struct Tiled {
     const int first_in_tile = 32 * (PAIRED ? wave >> 1 : wave), in_tile = first_in_tile + (int)c;
     const int rows = rq.n * a.G, first_row = tile.row0 + first_in_tile, row = tile.row0 + in_tile;
     const bool on = row < rows, any = first_row < rows;
-    const int node = on ? row / a.G : 0, hq = tile.h * a.G + (on ? row - node * a.G : 0);
+    const int node = on ? node_of(a, row) : 0, hq = tile.h * a.G + (on ? row - node * a.G : 0);
     constexpr int KT = PAIRED ? KB / 64 : KB / 32;
     Wave<KT> w;
     // a negative scale turns the queries round, so that the largest product
@@ -469,9 +469,9 @@ struct Tiled {
     const int32_t *table = a.table + (size_t)tile.r * a.blocks;
     // places from here on: some rows of the tile (of this wave) do not see them; none of the wave's does
     const int ctx = rq.len - rq.n;
-    const int tile_from = a.mask ? ctx : ctx + tile.row0 / a.G + 1;
-    const int from = a.mask || !any ? ctx : ctx + first_row / a.G + 1;
-    const int until = !any ? 0 : a.mask ? rq.len : ctx + (min(first_row + 31, rows - 1)) / a.G + 1;
+    const int tile_from = a.mask ? ctx : ctx + node_of(a, tile.row0) + 1;
+    const int from = a.mask || !any ? ctx : ctx + node_of(a, first_row) + 1;
+    const int until = !any ? 0 : a.mask ? rq.len : ctx + node_of(a, min(first_row + 31, rows - 1)) + 1;
     const int end = min(hi * KB, rq.len);
     const int half = PAIRED ? 32 * KT * (wave & 1) : 0, late_wave = kPhases && wave >= NW / 2;
     lds_char *buf = (lds_char *)L.buf, *ring = buf + kBuffers * kBuffer;

@@ -43,8 +43,11 @@ struct AttnArgs {
   float *lse, *part;  // part: the partial results of split tiles, of up to part_rows rows
   float scale;
   int dtype, T, Hq, G, blocks, R, words, part_rows;
-  uint32_t page_magic;  // a place p < 2^31 is in block umulhi(2p, page_magic) >> page_shift
-  int page_shift;
+  // x / d for x < 2^31 is umulhi(2x, magic) >> shift: places by page_size, rows by G
+  uint32_t page_magic, group_magic;
+  int page_shift, group_shift;
+  int slope;        // 16 tile_rows / G
+  double inv_groups;  // 1 / workgroups of the launch
 };
 int attn_tile_rows(int T, int G, int R, int D);
 int attn_workgroups(int tile_rows);

@@ -311,13 +311,20 @@ k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T, i
   a.blocks = blocks;
   a.R = R;
   a.words = words;
-  a.part_rows = attn_part_rows(attn_tile_rows(T, a.G, R, D), T, a.G);
-  // p / P = (p * m) >> (31 + s) for p < 2^31: s = ceil(log2 P), m the next
-  // integer above 2^(31 + s) / P (m < 2^32, and m P - 2^(31 + s) <= 2^s)
-  int shift = 0;
-  while ((1ll << shift) < cache->page_size) shift++;
-  a.page_shift = shift;
-  a.page_magic = (uint32_t)(((uint64_t)1 << (31 + shift)) / cache->page_size + 1);
+  // x / d = (x * m) >> (31 + s) for x < 2^31: s = ceil(log2 d), m the next
+  // integer above 2^(31 + s) / d (m < 2^32, and m d - 2^(31 + s) <= 2^s)
+  auto divisor = [](int d, uint32_t *magic, int *shift) {
+    int s = 0;
+    while ((1ll << s) < d) s++;
+    *shift = s;
+    *magic = (uint32_t)(((uint64_t)1 << (31 + s)) / d + 1);
+  };
+  divisor(cache->page_size, &a.page_magic, &a.page_shift);
+  divisor(a.G, &a.group_magic, &a.group_shift);
+  const int tile_rows = attn_tile_rows(T, a.G, R, D);
+  a.part_rows = attn_part_rows(tile_rows, T, a.G);
+  a.slope = 16 * tile_rows / a.G;
+  a.inv_groups = 1.0 / attn_workgroups(tile_rows);
   return device_status(launch_tree_attention(a, stream), fn);
 }
 
