@@ -2,8 +2,9 @@
 //
 // The keys and values are read once and bound the time, so they go from
 // memory into registers, without shared memory or barriers on the way: each
-// of a workgroup's four waves takes every fourth run of 32 places, and the
-// waves' results meet at the tile's end. Everything is transposed, so that no
+// of a workgroup's four waves takes every fourth run of 32 places (two runs at
+// once of short e4m3 rows, for as many bytes under way), and the waves'
+// results meet at the tile's end. Everything is transposed, so that no
 // value crosses lanes between the two products (lane l, c = l % 16, g = l / 16):
 //   S^T = K Q^T   rows: 2 x 16 places, columns: 16 rows of the tile.
 //                 K from memory in the operand's layout (lane: place c, 8
@@ -23,7 +24,7 @@
 //
 // Measured: one token of each of 64 requests of up to 8191 places, 8 key heads
 // of 128 in bf16, 1.09 GB: 188 us, 5.7 TB/s (a copy on this card moves 5.0, a
-// plain read up to 7.0); in e4m3 115 us.
+// plain read up to 7.0); in e4m3 109 us.
 #pragma once
 
 #include "k3_attn.h"
@@ -31,29 +32,35 @@
 namespace k3 {
 
 constexpr int kStreamWaves = 4, kStreamThreads = 64 * kStreamWaves;
-constexpr int kStreamKeys = 32 * kStreamWaves;  // KB: a unit's places
+// Runs of 32 places that a wave loads at once: two of e4m3 rows where they are
+// short (64 requests of up to 8191 places: 113 -> 109 us at a head of 128, 75 ->
+// 68 at 64; 16-bit rows of 64 gain nothing).
+template <bool F8, int D>
+constexpr int kStreamRuns = F8 && D <= 128 ? 2 : 1;
 
 // BF: bf16 (else fp16) queries, outputs and weights; F8: the cache is e4m3.
 template <bool BF, bool F8, int D, int QT>
 struct Stream {
   static constexpr int RT = 16 * QT, NS = D / 32, DPL = D / 16;
   static constexpr int ES = F8 ? 1 : 2;
+  static constexpr int RUNS = kStreamRuns<F8, D>, PLACES = 32 * RUNS;
+  static constexpr int KB = PLACES * kStreamWaves;  // a block's places
   static constexpr int VW = DPL * ES / 4;     // words of a row of V per lane
   static constexpr int KW = F8 ? 2 : 4;       // words of a K operand
   static constexpr int kPad = D + 4;
   struct Lds {
-    int64_t offset[kStreamWaves][32];
+    int64_t offset[kStreamWaves][PLACES];
     float ml[kStreamWaves][2][RT];
     float o[kStreamWaves][16 * kPad];
   };
 
   struct Wave {
     u32x4 q[QT][NS];
-    uint32_t k[2][NS][KW];
-    uint32_t v[8][VW];
+    uint32_t k[RUNS][2][NS][KW];
+    uint32_t v[RUNS][8][VW];
     f32x4 o[QT][DPL];
     float ref[QT], sum[QT];  // the reference exponent, this lane's part of the sum
-    uint32_t present;
+    uint32_t present[RUNS];
   };
 
   // Value d of the head that element j of step s holds in lane group g.
@@ -67,17 +74,20 @@ struct Stream {
     return b < (uint32_t)a.blocks ? row[b] : -1;
   }
 
-  // The 32 places from k0 on: this lane's (lane % 32) page is `page`. Leaves
+  // The places from k0 on: this lane's (lane % PLACES) page is `page`. Leaves
   // the rows' offsets in LDS; places that are not there read row 0.
-  static __device__ __forceinline__ uint32_t places(const AttnArgs &a, int64_t *offset, int lane, int k0, int page) {
-    const int p = k0 + (lane & 31);
+  static __device__ __forceinline__ void places(const AttnArgs &a, Wave &w, int64_t *offset, int lane, int k0,
+                                                int page) {
+    const int p = k0 + lane % PLACES;
     const bool there = page >= 0 && page < a.c.n_pages;
     const uint32_t b = __umulhi(2u * (uint32_t)p, a.page_magic) >> a.page_shift;
     const int64_t at = page * a.c.page_stride + (int)((uint32_t)p - b * a.c.page_size) * a.c.slot_stride;
     wave_sync();  // the last run's readers are done
-    if (lane < 32) offset[lane] = there ? at * ES : 0;
+    if (lane < PLACES) offset[lane] = there ? at * ES : 0;
     wave_sync();
-    return (uint32_t)__ballot(there);
+    const uint64_t all = __ballot(there);
+#pragma unroll
+    for (int r = 0; r < RUNS; r++) w.present[r] = (uint32_t)(all >> (32 * r));
   }
 
   // Keys and values are read once, so they pass the caches by (not kept there
@@ -87,25 +97,25 @@ struct Stream {
     return __builtin_nontemporal_load((const T *)p);
   }
 
-  static __device__ __forceinline__ void load_k(Wave &w, const char *k, const int64_t *offset, int c, int g) {
+  static __device__ __forceinline__ void load_k(Wave &w, const char *k, const int64_t *offset, int r, int c, int g) {
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-      const char *p = k + offset[16 * u + c];
+      const char *p = k + offset[32 * r + 16 * u + c];
       if (F8) {
 #pragma unroll
         for (int s = 0; s < NS; s += 2) {
           const u32x4 x = read_once<u32x4>(p + d_of(s, g));
-          w.k[u][s][0] = x[0];
-          w.k[u][s][1] = x[1];
-          w.k[u][s + 1][0] = x[2];
-          w.k[u][s + 1][1] = x[3];
+          w.k[r][u][s][0] = x[0];
+          w.k[r][u][s][1] = x[1];
+          w.k[r][u][s + 1][0] = x[2];
+          w.k[r][u][s + 1][1] = x[3];
         }
       } else {
 #pragma unroll
         for (int s = 0; s < NS; s++) {
           const u32x4 x = read_once<u32x4>(p + 2 * d_of(s, g));
 #pragma unroll
-          for (int i = 0; i < KW; i++) w.k[u][s][i] = x[i];
+          for (int i = 0; i < KW; i++) w.k[r][u][s][i] = x[i];
         }
       }
     }
@@ -116,43 +126,51 @@ struct Stream {
   static constexpr int kRun = DPL < 16 / ES ? DPL : 16 / ES;
   static __device__ __forceinline__ int value_of(int c, int e) { return 16 * kRun * (e / kRun) + kRun * c + e % kRun; }
 
-  static __device__ __forceinline__ void load_v(Wave &w, const char *v, const int64_t *offset, int c, int g) {
+  static __device__ __forceinline__ void load_v(Wave &w, const char *v, const int64_t *offset, int r, int c, int g) {
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      const char *p = v + offset[16 * (j / 4) + 4 * g + j % 4];
+      const char *p = v + offset[32 * r + 16 * (j / 4) + 4 * g + j % 4];
       if constexpr (VW == 1) {
-        w.v[j][0] = read_once<uint32_t>(p + c * 4);
+        w.v[r][j][0] = read_once<uint32_t>(p + c * 4);
       } else if constexpr (VW == 2) {
         const u32x2 x = read_once<u32x2>(p + c * 8);
-        w.v[j][0] = x[0];
-        w.v[j][1] = x[1];
+        w.v[r][j][0] = x[0];
+        w.v[r][j][1] = x[1];
       } else {
 #pragma unroll
         for (int i = 0; i < VW; i += 4) {
           const u32x4 x = read_once<u32x4>(p + 64 * i + c * 16);
 #pragma unroll
-          for (int e = 0; e < 4; e++) w.v[j][i + e] = x[e];
+          for (int e = 0; e < 4; e++) w.v[r][j][i + e] = x[e];
         }
       }
     }
   }
 
-  static __device__ __forceinline__ u32x4 k_operand(const Wave &w, int u, int s) {
+  static __device__ __forceinline__ void load(Wave &w, const char *k, const char *v, const int64_t *offset, int c,
+                                              int g) {
+#pragma unroll
+    for (int r = 0; r < RUNS; r++) load_k(w, k, offset, r, c, g);
+#pragma unroll
+    for (int r = 0; r < RUNS; r++) load_v(w, v, offset, r, c, g);
+  }
+
+  static __device__ __forceinline__ u32x4 k_operand(const uint32_t (&k)[2][NS][KW], int u, int s) {
     if constexpr (F8)
-      return u32x4{widen2<BF, false>(w.k[u][s][0]), widen2<BF, true>(w.k[u][s][0]), widen2<BF, false>(w.k[u][s][1]),
-                   widen2<BF, true>(w.k[u][s][1])};
+      return u32x4{widen2<BF, false>(k[u][s][0]), widen2<BF, true>(k[u][s][0]), widen2<BF, false>(k[u][s][1]),
+                   widen2<BF, true>(k[u][s][1])};
     else
-      return u32x4{w.k[u][s][0], w.k[u][s][1], w.k[u][s][2], w.k[u][s][3]};
+      return u32x4{k[u][s][0], k[u][s][1], k[u][s][2], k[u][s][3]};
   }
 
   // V^T operands of the values 4 / ES that word i of the lane's row parts hold.
   template <class F>
-  static __device__ __forceinline__ void v_operands(const Wave &w, int i, F &&use) {
+  static __device__ __forceinline__ void v_operands(const uint32_t (&v)[8][VW], int i, F &&use) {
     if constexpr (F8) {
       uint32_t t[4][2];  // [value][places 0..3, 4..7] as four bytes
 #pragma unroll
       for (int x = 0; x < 2; x++) {
-        const uint32_t a = w.v[4 * x][i], b = w.v[4 * x + 1][i], c = w.v[4 * x + 2][i], d = w.v[4 * x + 3][i];
+        const uint32_t a = v[4 * x][i], b = v[4 * x + 1][i], c = v[4 * x + 2][i], d = v[4 * x + 3][i];
         const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x05010400), cd = __builtin_amdgcn_perm(d, c, 0x05010400);
         const uint32_t AB = __builtin_amdgcn_perm(b, a, 0x07030602), CD = __builtin_amdgcn_perm(d, c, 0x07030602);
         t[0][x] = __builtin_amdgcn_perm(cd, ab, 0x05040100);
@@ -168,8 +186,8 @@ struct Stream {
       u32x4 lo, hi;
 #pragma unroll
       for (int x = 0; x < 4; x++) {
-        lo[x] = __builtin_amdgcn_perm(w.v[2 * x + 1][i], w.v[2 * x][i], 0x05040100);
-        hi[x] = __builtin_amdgcn_perm(w.v[2 * x + 1][i], w.v[2 * x][i], 0x07060302);
+        lo[x] = __builtin_amdgcn_perm(v[2 * x + 1][i], v[2 * x][i], 0x05040100);
+        hi[x] = __builtin_amdgcn_perm(v[2 * x + 1][i], v[2 * x][i], 0x07060302);
       }
       use(2 * i, lo);
       use(2 * i + 1, hi);
@@ -221,6 +239,7 @@ struct Stream {
   }
 
   // One run of 32 places: scores, weights, and the weighted values.
+  template <int RUN>
   static __device__ __forceinline__ void run(const AttnArgs &a, Wave &w, const Request &rq, const int *node, int k0,
                                              float scale, const char *v, const int64_t *offset, float *scratch, int c,
                                              int g) {
@@ -233,11 +252,11 @@ struct Stream {
     for (int i = 0; i < NS; i++)
 #pragma unroll
       for (int u = 0; u < 2; u++) {
-        const u32x4 k = k_operand(w, u, i);
+        const u32x4 k = k_operand(w.k[RUN], u, i);
 #pragma unroll
         for (int t = 0; t < QT; t++) s[t][u] = mfma16<BF>(k, w.q[t][i], s[t][u]);
       }
-    const uint32_t present = w.present;
+    const uint32_t present = w.present[RUN];
     const bool drafts = k0 + 32 > rq.len - rq.n, partial = drafts || present != 0xffffffffu;
     bool odd = false;
     if (partial) {
@@ -246,7 +265,7 @@ struct Stream {
         for (int j = 0; j < 8; j++)
           if (!((present >> (16 * (j / 4) + 4 * g + j % 4)) & 1))
 #pragma unroll
-            for (int i = 0; i < VW; i++) w.v[j][i] = 0;
+            for (int i = 0; i < VW; i++) w.v[RUN][j][i] = 0;
       }
       if (drafts) {
         uint32_t lost = 0;
@@ -254,9 +273,9 @@ struct Stream {
         for (int j = 0; j < 8; j++)
 #pragma unroll
           for (int i = 0; i < VW; i++) {
-            const uint32_t f = finite(w.v[j][i]);
-            lost |= f ^ w.v[j][i];
-            w.v[j][i] = f;
+            const uint32_t f = finite(w.v[RUN][j][i]);
+            lost |= f ^ w.v[RUN][j][i];
+            w.v[RUN][j][i] = f;
           }
         odd = __ballot(lost != 0) != 0;
       }
@@ -300,7 +319,7 @@ struct Stream {
     }
 #pragma unroll
     for (int i = 0; i < VW; i++)
-      v_operands(w, i, [&](int e, u32x4 operand) {
+      v_operands(w.v[RUN], i, [&](int e, u32x4 operand) {
 #pragma unroll
         for (int t = 0; t < QT; t++) w.o[t][e] = mfma16<BF>(operand, p[t], w.o[t][e]);
       });
@@ -333,21 +352,21 @@ struct Stream {
     const char *v = (const char *)a.c.v + tile.h * a.c.head_stride * ES;
     const int32_t *table = a.table + (size_t)tile.r * a.blocks;
     int64_t *offset = L.offset[wave];
-    const int end = (int)min((long long)hi * kStreamKeys, (long long)tile.places);
-    int k0 = lo * kStreamKeys + 32 * wave;
-    int page = table_entry(a, table, k0 + (lane & 31), rq.len);
+    const int end = (int)min((long long)hi * KB, (long long)tile.places);
+    int k0 = lo * KB + PLACES * wave;
+    int page = table_entry(a, table, k0 + lane % PLACES, rq.len);
     if (k0 < end) {
-      w.present = places(a, offset, lane, k0, page);
-      load_k(w, k, offset, c, g);
-      load_v(w, v, offset, c, g);
-      page = table_entry(a, table, k0 + kStreamKeys + (lane & 31), rq.len);
-      for (; k0 < end; k0 += kStreamKeys) {
-        run(a, w, rq, node, k0, scale, v, offset, L.o[wave], c, g);
-        if (k0 + kStreamKeys < end) {
-          w.present = places(a, offset, lane, k0 + kStreamKeys, page);
-          page = table_entry(a, table, k0 + 2 * kStreamKeys + (lane & 31), rq.len);
-          load_k(w, k, offset, c, g);
-          load_v(w, v, offset, c, g);
+      places(a, w, offset, lane, k0, page);
+      load(w, k, v, offset, c, g);
+      page = table_entry(a, table, k0 + KB + lane % PLACES, rq.len);
+      for (; k0 < end; k0 += KB) {
+        run<0>(a, w, rq, node, k0, scale, v, offset, L.o[wave], c, g);
+        if (RUNS > 1 && k0 + 32 < end)
+          run<RUNS - 1>(a, w, rq, node, k0 + 32, scale, v, offset + PLACES - 32, L.o[wave], c, g);
+        if (k0 + KB < end) {
+          places(a, w, offset, lane, k0 + KB, page);
+          page = table_entry(a, table, k0 + 2 * KB + lane % PLACES, rq.len);
+          load(w, k, v, offset, c, g);
         }
       }
     }
@@ -423,7 +442,7 @@ template <bool BF, bool F8, int D, int QT>
 __global__ __launch_bounds__(kStreamThreads) void attn_stream_kernel(AttnArgs a) {
   using S = Stream<BF, F8, D, QT>;
   __shared__ typename S::Lds L;
-  walk<S::RT, kStreamKeys, 0, D, kStreamThreads>(a, [&](const Tile &tile, int lo, int hi, int slot) {
+  walk<S::RT, S::KB, 0, D, kStreamThreads>(a, [&](const Tile &tile, int lo, int hi, int slot) {
     S::segment(a, L, tile, lo, hi, slot, gridDim.x);
   });
 }
