@@ -16,14 +16,14 @@ hipError_t launch_join(const AttnArgs &a, int B, hipStream_t s) {
 
 template <bool BF, bool F8, int D, int QT>
 hipError_t launch_stream(const AttnArgs &a, hipStream_t s) {
-  const int B = attn_workgroups(16 * QT);
+  const int B = attn_workgroups(16 * QT, D);
   attn_stream_kernel<BF, F8, D, QT><<<B, kStreamThreads, 0, s>>>(a);
   return launch_join<BF, D>(a, B, s);
 }
 
 template <bool BF, bool F8, int D>
 hipError_t launch_tile(const AttnArgs &a, hipStream_t s) {
-  const int B = attn_workgroups(32 * kAttnWaves<D>);
+  const int B = attn_workgroups(32 * kAttnWaves<D>, D);
   attn_tile_kernel<BF, F8, D><<<B, kAttnThreads<D>, 0, s>>>(a);
   return launch_join<BF, D>(a, B, s);
 }

@@ -50,7 +50,7 @@ struct AttnArgs {
   double inv_groups;  // 1 / workgroups of the launch
 };
 int attn_tile_rows(int T, int G, int R, int D);
-int attn_workgroups(int tile_rows);
+int attn_workgroups(int tile_rows, int D);
 size_t attn_workspace_bytes(int T, int Hq, int n_heads, int D);
 hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t s);
 

@@ -31,20 +31,22 @@ int attn_tile_rows(int T, int G, int R, int D) {
   return rows <= 32 ? 32 : 256;
 }
 
-// Two workgroups of the streaming kernel's 16-row tiles fit on a CU, one of
-// the others.
-int attn_workgroups(int tile_rows) {
+// Two workgroups of the streaming kernel's 16-row tiles fit on a CU (one at a
+// head of 256), one of the others.
+int attn_workgroups(int tile_rows, int D) {
   const int cus = std::min(num_cus(), kMaxWorkgroups / 2);
-  return tile_rows == 16 ? 2 * cus : cus;
+  return tile_rows == 16 && D < 256 ? 2 * cus : cus;
 }
 
 static int attn_part_rows(int tile_rows, int T, int G) { return (int)std::min((long long)tile_rows, (long long)T * G); }
 
 size_t attn_workspace_bytes(int T, int Hq, int n_heads, int D) {
-  // R is not known here, and more requests only make the tiles smaller
-  const int G = Hq / n_heads, rows = attn_tile_rows(T, G, 1, D);
-  return (size_t)2 * attn_workgroups(rows) * attn_part_rows(rows, T, G) * (D + 2) * sizeof(float) +
-         kMaxWorkgroups * sizeof(JoinJob);
+  // R is not known here: any tile up to the one request's may be taken
+  const int G = Hq / n_heads, largest = attn_tile_rows(T, G, 1, D);
+  size_t rows = 0;
+  for (int r : {16, 32, 128, 256})
+    if (r <= largest) rows = std::max(rows, (size_t)2 * attn_workgroups(r, D) * attn_part_rows(r, T, G));
+  return rows * (D + 2) * sizeof(float) + kMaxWorkgroups * sizeof(JoinJob);
 }
 
 hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t s) {
@@ -324,7 +326,7 @@ k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T, i
   const int tile_rows = attn_tile_rows(T, a.G, R, D);
   a.part_rows = attn_part_rows(tile_rows, T, a.G);
   a.slope = 16 * tile_rows / a.G;
-  a.inv_groups = 1.0 / attn_workgroups(tile_rows);
+  a.inv_groups = 1.0 / attn_workgroups(tile_rows, D);
   return device_status(launch_tree_attention(a, stream), fn);
 }
 

@@ -67,7 +67,10 @@ def test_many_requests(R, every, n, G, H):
 @pytest.mark.parametrize("ctx,new,H,G,D,cache", [
     ([700], [1], 2, 8, 128, "bf16"), ([700], [4], 2, 8, 128, "e4m3"), ([3000, 9], [40, 3], 2, 8, 128, "bf16"),
     ([3000, 20, 100, 9], [60, 4, 4, 4], 1, 8, 64, "bf16"), ([900], [60], 2, 8, 256, "bf16"),
-    ([100] * 20, [1] * 20, 1, 3, 64, "bf16")])
+    ([100] * 20, [1] * 20, 1, 3, 64, "bf16"),
+    # as one request these rows would make a larger tile on fewer workgroups
+    ([9000] * 2, [1] * 2, 2, 10, 128, "bf16"), ([9000] * 3, [1] * 3, 2, 8, 64, "bf16"),
+    ([5000] * 2, [1] * 2, 2, 9, 256, "bf16"), ([9000] * 3, [2] * 3, 2, 8, 128, "e4m3")])
 def test_workspace_is_as_large_as_said(ctx, new, H, G, D, cache):
     """Nothing past it is written, and what it held before does not matter."""
     import torch
