@@ -150,7 +150,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
 // Workgroups of the launch: four rows each of the tiles that may be split, up
 // to four for each CU, which run at once, and never fewer than those tiles.
 inline int join_workgroups(const AttnArgs &a, int B) {
-  const long long tiles = std::min<long long>(B, (a.R + (long long)a.T * a.G / a.part_rows) * a.c.n_heads);
+  const long long tiles = std::min<long long>(B, (1 + (long long)a.T * a.G / a.part_rows) * a.R * a.c.n_heads);
   return (int)std::min<long long>(std::max(B, 4 * num_cus()), tiles * ((a.part_rows + kJoinWaves - 1) / kJoinWaves));
 }
 

@@ -452,18 +452,18 @@ struct Tiled {
     constexpr int KT = PAIRED ? KB / 64 : KB / 32;
     Wave<KT> w;
     // a negative scale turns the queries round, so that the largest product
-    // has the largest score
-    const uint32_t round = a.scale < 0.f ? 0x80008000u : 0u;
+    // has the largest score; at 0 every product is 0
+    const float factor = a.scale * (a.c.k_scale ? a.c.k_scale[tile.h] : 1.f) * kLog2e;
+    const uint32_t round = factor < 0.f ? 0x80008000u : 0u;
+    const float scale = factor == 0.f ? 1.f : fabsf(factor);
     const uint16_t *q = a.q + (int64_t)(rq.t0 + node) * a.q_stride + hq * D + 8 * h;
 #pragma unroll
     for (int s = 0; s < NS; s++)
-      w.q[s] = on && a.scale != 0.f ? *(const u32x4 *)(q + 16 * s) : u32x4{0, 0, 0, 0};
+      w.q[s] = on && factor != 0.f ? *(const u32x4 *)(q + 16 * s) : u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int t = 0; t < DT; t++) w.o[t] = f32x16{};
     w.ref = -INFINITY;
     w.sum = 0.f;
-    const float k_scale = a.c.k_scale ? a.c.k_scale[tile.h] : 1.f;
-    const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale) * k_scale * kLog2e;
     const char *k = (const char *)a.c.k + tile.h * a.c.head_stride * ES;
     const char *v = (const char *)a.c.v + tile.h * a.c.head_stride * ES;
     const int32_t *table = a.table + (size_t)tile.r * a.blocks;

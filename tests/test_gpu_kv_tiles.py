@@ -103,3 +103,73 @@ def test_rows_without_a_number_keep_to_themselves(D, G, n):
     same[1, 0] = same[n, G - 1] = False
     assert torch.equal(got[same], want[same]) and torch.equal(l2[same], lse[same])
     assert got[1, 0].isnan().all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,G", [(20, 8), (1, 8), (9, 3)])
+def test_key_scales_of_any_sign(D, n, G):
+    """A head's scale may be 0 (all its scores are) or negative, and so may the call's."""
+    import torch
+    say(f"key scales D={D} n={n} G={G}")
+    s = kv.attn_case([130, 3], [n, n], 3, G, D, "bf16", "e4m3", 16, 5)
+    s["ks"].copy_(torch.tensor([0.0, -0.02, 0.02], device="cuda"))
+    kv.check_attn(s)
+    s["scale"] = -s["scale"]
+    kv.check_attn(s)
+
+
+@pytest.mark.parametrize("D,cache", [(128, "bf16"), (64, "e4m3"), (256, "bf16")])
+def test_graph_of_tiles(D, cache):
+    """Captured once, replayed with other lengths and rows between eager calls: the same bits."""
+    import torch
+    say(f"graph of tiles D={D} {cache}")
+    T, H, G, n = 60, 2, 8, 20
+    cases = [kv.attn_case(ctx, [n] * 3, H, G, D, "bf16", cache, 16, i) for i, ctx in
+             enumerate(([900, 5, 300], [64, 640, 0], [1000, 1000, 1]))]
+    pages, blocks = max(c["pages"] for c in cases), max(c["table"].shape[1] for c in cases)
+    like = lambda x: torch.zeros((pages, H, 16, D), device="cuda").to(x.dtype).permute(0, 2, 1, 3)  # noqa: E731
+    kc, vc = like(cases[0]["kc"]), like(cases[0]["vc"])
+    scales = [None if cases[0][x] is None else cases[0][x].clone() for x in ("ks", "vs")]
+    q, out = (torch.zeros((T, H * G, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lse = torch.zeros((T, H * G), device="cuda")
+    table, cu, lens = R_.i32(np.zeros((3, blocks))), R_.i32(np.arange(4) * n), R_.i32([0] * 3)
+    mask = R_.i32(np.zeros((T, 1)))
+    ws = torch.empty(K.k3_tree_attention_workspace_bytes(T, H * G, H, D), dtype=torch.uint8, device="cuda")
+    handle = K.k3_kv_cache_of(kc, vc, *scales)
+
+    def call():
+        K.k3_tree_attention(q, T, H * G, handle, table, blocks, cu, lens, 3, mask, 1, D ** -0.5, out, ws, lse=lse)
+
+    def load(c):
+        raw = torch.uint8 if cache == "e4m3" else torch.int16
+        for to, x in ((kc, c["kc"]), (vc, c["vc"])):
+            to.view(raw)[:c["pages"]] = x.view(raw)
+        for to, x in zip(scales, (c["ks"], c["vs"])):
+            if to is not None:
+                to.copy_(x)
+        q.copy_(c["q"])
+        t = np.full((3, blocks), -1)
+        t[:, :c["table"].shape[1]] = c["table"]
+        table.copy_(R_.i32(t))
+        lens.copy_(R_.i32(c["lens"]))
+        mask.copy_(R_.i32(c["mask"]))
+        out.zero_()
+        torch.cuda.synchronize()
+
+    load(cases[0])
+    call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for i in (1, 2, 0, 1):
+        load(cases[i])
+        call()
+        torch.cuda.synchronize()
+        want = out.clone(), lse.clone()
+        load(cases[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        R_.check_attention(out, lse, kv.reference(cases[i]), "bf16", int(max(cases[i]["lens"])))
