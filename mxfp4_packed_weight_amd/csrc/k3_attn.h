@@ -105,6 +105,7 @@ struct Cost {
 template <int THREADS>
 struct Line {
   long long pre[THREADS + 1], wave_sum[THREADS / 64];
+  Request request[THREADS];  // the last of each thread's
 };
 template <int THREADS>
 __device__ __forceinline__ int run_of(int R) { return (R + THREADS - 1) / THREADS; }
@@ -113,7 +114,11 @@ template <int RT, int HALF, int THREADS>
 __device__ __forceinline__ void line_of_tiles(const AttnArgs &a, Line<THREADS> &L) {
   const int tid = threadIdx.x, lane = tid & 63, per = run_of<THREADS>(a.R);
   long long own = 0;
-  for (int r = tid * per; r < min(a.R, tid * per + per); r++) own += Cost<RT, HALF>(a, request_of(a, r)).of_request(a);
+  for (int r = tid * per; r < min(a.R, tid * per + per); r++) {
+    const Request q = request_of(a, r);
+    own += Cost<RT, HALF>(a, q).of_request(a);
+    L.request[tid] = q;
+  }
   long long incl = own;
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) {
@@ -133,6 +138,15 @@ __device__ __forceinline__ void line_of_tiles(const AttnArgs &a, Line<THREADS> &
 __device__ __forceinline__ long long in_all_lanes(long long x) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)x), hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
   return (long long)((uint64_t)hi << 32 | lo);
+}
+
+// Request r again: out of LDS where each thread has one.
+template <int THREADS>
+__device__ __forceinline__ Request request_again(const AttnArgs &a, const Line<THREADS> &L, int r) {
+  if (a.R > THREADS) return request_of(a, r);
+  const Request &q = L.request[r];
+  return {__builtin_amdgcn_readfirstlane(q.t0), __builtin_amdgcn_readfirstlane(q.n),
+          __builtin_amdgcn_readfirstlane(q.len)};
 }
 
 // A tile in the line.
@@ -171,12 +185,12 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &
   }
   long long before = in_all_lanes(L.pre[run]);
   t.r = run * per;
-  t.q = request_of(a, t.r);
+  t.q = request_again(a, L, t.r);
   for (; t.r + 1 < min(a.R, run * per + per); t.r++) {
     const long long all = Cost<RT, HALF>(a, t.q).of_request(a);
     if (before + all > u) break;
     before += all;
-    t.q = request_of(a, t.r + 1);
+    t.q = request_again(a, L, t.r + 1);
   }
   const Cost<RT, HALF> cost(a, t.q);
   // (the product is off by less than 1: n_heads <= 2^10)
@@ -197,14 +211,14 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &
   return t;
 }
 // The next tile (there is one).
-template <int RT, int KB, int HALF>
-__device__ __forceinline__ void next_tile(const AttnArgs &a, Tile &t) {
+template <int RT, int KB, int HALF, int THREADS>
+__device__ __forceinline__ void next_tile(const AttnArgs &a, const Line<THREADS> &L, Tile &t) {
   t.first = t.after;
   if (++t.x == t.tiles) {
     t.x = 0;
     if (++t.h == a.c.n_heads) {
       t.h = 0;
-      do t.q = request_of(a, ++t.r);
+      do t.q = request_again(a, L, ++t.r);
       while (t.q.n == 0 && t.r + 1 < a.R);
     }
   }
@@ -273,7 +287,7 @@ __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
   Tile tile;
   for (long long u = begin; u < end;) {
     if (u == begin) tile = tile_at<RT, KB, HALF>(a, L, u);
-    else next_tile<RT, KB, HALF>(a, tile);
+    else next_tile<RT, KB, HALF>(a, L, tile);
     const int lo = block_from<RT, KB>(tile, u), hi = block_from<RT, KB>(tile, end);
     const int slot = lo == hi || (lo == 0 && hi == tile.blocks) ? -1 : lo ? 2 * b : 2 * b + 1;
     if (u > tile.first) job.head_slot = slot;
