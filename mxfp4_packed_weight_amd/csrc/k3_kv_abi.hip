@@ -20,9 +20,9 @@ hipError_t launch_attn_f16_e4m3(const AttnArgs &a, hipStream_t s);
 // 32 requests of 8192 places, us:
 //   rows             16          32          48
 //   128, bf16     175 / 197   177 / 197   343 / 198
-//   128, e4m3     100 / 140   124 / 141   239 / 156
+//   128, e4m3     100 / 140   119 / 141   239 / 156
 //    64, bf16      95 / 104   103 / 104   197 / 107
-//   256, bf16     195 / 205   318 / 207   563 / 212
+//   256, bf16     196 / 205   318 / 207   563 / 212
 // and 63 requests of one token with one of 512, 8 rows to a node: 381 / 224.
 int attn_tile_rows(int T, int G, int R, int D) {
   const long long rows = ((long long)T * G + R - 1) / R;
