@@ -711,8 +711,9 @@ k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T,
  * = ctx[r] + n_accepted[r]. accepted [R][most]: node indices in strictly
  * ascending order. Layer l's cache is at cache->k + l * layer_stride (and v
  * alike, elements). A request with n_accepted outside [0, most], indices
- * that do not ascend from >= 0, or a row to move whose place has no page,
- * stays as it is, with ctx_out[r] = ctx[r]. ctx_out is apart from ctx. */
+ * that do not ascend from >= 0, or a place ctx[r] + accepted[r][i] or ctx[r] +
+ * i that has no page (rows that stay where they are included) stays as it
+ * is, with ctx_out[r] = ctx[r]. ctx_out is apart from the inputs. */
 k3_status k3_kv_commit(const k3_kv_cache *cache, int layers, int64_t layer_stride,
                        const int32_t *table, int blocks, const int32_t *ctx,
                        const int32_t *accepted, const int32_t *n_accepted,

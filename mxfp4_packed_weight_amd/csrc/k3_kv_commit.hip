@@ -41,18 +41,17 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(KvCommitArgs 
   __syncthreads();
   for (int i = tid; i < todo; i += kCommitThreads) {
     const int from = acc[i], before = i ? acc[i - 1] : -1;
-    int64_t s_at = 0, d_at = 0;
-    if (from <= before) {  // before >= -1: not ascending, or below zero
-      bad = 1;
-    } else if (from != i) {
+    int64_t s_at = -1, d_at = -1;
+    if (from > before) {  // before >= -1: ascending, and not below zero
       s_at = place_offset(a, row, (int64_t)ctx + from, es);
-      d_at = place_offset(a, row, (int64_t)ctx + i, es);
-      if (s_at < 0 || d_at < 0) bad = 1;
+      d_at = from == i ? s_at : place_offset(a, row, (int64_t)ctx + i, es);
     }
-    src[i] = s_at;
-    dst[i] = d_at;
+    if (s_at < 0 || d_at < 0) bad = 1;
+    src[i] = from == i ? 0 : s_at;
+    dst[i] = from == i ? 0 : d_at;
   }
   __syncthreads();
+  // (all n places are in the table's row, so the sum is at most 2^30)
   if (layer == 0 && tid == 0) a.ctx_out[r] = bad ? ctx : ctx + n;
   if (bad) return;
   const int per_head = row16, cols = a.c.n_heads * per_head;
