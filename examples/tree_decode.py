@@ -5,7 +5,7 @@ Each step drafts a tree per request out of what followed the last token
 before, plans the step on the device (k3_kv_plan), and for each layer appends
 and attends (k3_qk_norm_rope, k3_tree_attention) and runs the routed experts
 (k3_moe_layer_batched). The drafts that greedy decoding would have chosen are
-kept (k3_kv_commit). At the end the whole sequences are run once more as
+kept (k3_kv_commit_ex). At the end the whole sequences are run once more as
 prompts, and the tokens compared with what that would have chosen.
 
     python examples/tree_decode.py [--requests 4] [--tokens 64] [--cache e4m3]
@@ -115,10 +115,10 @@ class Cache:
         self.held, self.ring_state = held, state
         return p
 
-    def commit(self, accepted, counts):
+    def commit(self, plan, accepted, counts):
         out = zeros(self.requests)
-        K.k3_kv_commit(self.layers[0], LAYERS, self.layer_stride, self.table, self.blocks, self.ctx, i32(accepted),
-                       i32(counts), len(accepted[0]), self.requests, out)
+        K.k3_kv_commit_ex(self.layers[0], LAYERS, self.layer_stride, self.table, self.blocks, self.ctx, plan.kv_lens,
+                          i32(accepted), i32(counts), len(accepted[0]), self.requests, out)
         self.ctx = out
 
 
@@ -187,7 +187,7 @@ def run(requests, tokens, nodes, kind, seed=0, log=print):
                 text[r].append(t)
             roots[r] = root
             first += len(toks)
-        cache.commit(accepted, counts)
+        cache.commit(plan, accepted, counts)
         steps += 1
         turns += sum(n > 0 for n in new)
     produced = sum(len(t) - p for t, p in zip(text, prompts))

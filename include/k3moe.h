@@ -576,7 +576,7 @@ k3_status k3_moe_layer_cached(const uint16_t *x, const uint16_t *router_w,
  * Paged key/value cache: the attention half of a decoding step, with drafted
  * trees. One step of a batch of R requests runs k3_kv_plan once, then for
  * each layer k3_qk_norm_rope (norm, rotation, append) and k3_tree_attention,
- * and, once the drafts are judged, k3_kv_commit over all layers.
+ * and, once the drafts are judged, k3_kv_commit_ex over all layers.
  *
  * Terms. Request r has ctx[r] committed tokens in the cache and new[r] tokens
  * in this step (one token, a prompt's chunk, or the nodes of a drafted tree
@@ -631,6 +631,8 @@ typedef struct k3_kv_cache {
  * pages to give back than the ring has room for (it asks for none and gives
  * none). `table` and `ring` are updated in place;
  * the others are outputs apart from the inputs:
+ * A row of the table keeps the ids of pages given back, past held_out[r];
+ * they are no longer the request's, and may be another's.
  *   held_out [R], ring_out [2]  the new held and ring_state
  *   cu [R + 1]                  prefix sums of new (negative ones count as
  *                               0; sums stop at 2^30)
@@ -713,11 +715,23 @@ k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T,
  * alike, elements). A request with n_accepted outside [0, most], indices
  * that do not ascend from >= 0, or a place ctx[r] + accepted[r][i] or ctx[r] +
  * i that has no page (rows that stay where they are included) stays as it
- * is, with ctx_out[r] = ctx[r]. ctx_out is apart from the inputs. */
+ * is, with ctx_out[r] = ctx[r]. ctx_out is apart from the inputs.
+ * k3_kv_commit_ex also takes the step's kv_lens, and leaves a request as it
+ * is if a place ctx[r] + accepted[r][i] is not below kv_lens[r]: one that the
+ * plan did not serve (kv_lens 0) keeps its length, whatever n_accepted says.
+ * k3_kv_commit cannot tell a request's pages from those that it gave back
+ * earlier: every id in range counts, and the caller sees to it that
+ * n_accepted is 0 for requests not served and that accepted names none but
+ * the step's nodes. */
 k3_status k3_kv_commit(const k3_kv_cache *cache, int layers, int64_t layer_stride,
                        const int32_t *table, int blocks, const int32_t *ctx,
                        const int32_t *accepted, const int32_t *n_accepted,
                        int most, int R, int32_t *ctx_out, k3_stream_t stream);
+k3_status k3_kv_commit_ex(const k3_kv_cache *cache, int layers, int64_t layer_stride,
+                          const int32_t *table, int blocks, const int32_t *ctx,
+                          const int32_t *kv_lens, const int32_t *accepted,
+                          const int32_t *n_accepted, int most, int R,
+                          int32_t *ctx_out, k3_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -121,6 +121,7 @@ SIGNATURES = [
     ("k3_tree_attention", _i, [_vp, _i64, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _i, _vp, _i,
                                ctypes.c_float, _vp, _i64, _vp, _sz, _vp, _vp]),
     ("k3_kv_commit", _i, [_vp, _i, _i64, _vp, _i, _vp, _vp, _vp, _i, _i, _vp, _vp]),
+    ("k3_kv_commit_ex", _i, [_vp, _i, _i64, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp]),
 ]
 
 
@@ -618,3 +619,10 @@ def k3_kv_commit(cache, layers, layer_stride, table, blocks, ctx, accepted, n_ac
                  ctx_out, stream=None):
     _call("k3_kv_commit", ctypes.byref(cache), layers, layer_stride, _ptr(table), blocks,
           _ptr(ctx), _ptr(accepted), _ptr(n_accepted), most, R, _ptr(ctx_out), _stream(stream))
+
+
+def k3_kv_commit_ex(cache, layers, layer_stride, table, blocks, ctx, kv_lens, accepted, n_accepted, most,
+                    R, ctx_out, stream=None):
+    _call("k3_kv_commit_ex", ctypes.byref(cache), layers, layer_stride, _ptr(table), blocks,
+          _ptr(ctx), _ptr(kv_lens), _ptr(accepted), _ptr(n_accepted), most, R, _ptr(ctx_out),
+          _stream(stream))

@@ -27,7 +27,7 @@ hipError_t launch_qk_norm_rope(const QkArgs &a, hipStream_t s);
 struct KvCommitArgs {
   k3_kv_cache c;
   int64_t layer_stride;
-  const int32_t *table, *ctx, *accepted, *n_accepted;
+  const int32_t *table, *ctx, *kv_lens, *accepted, *n_accepted;  // kv_lens may be null
   int32_t *ctx_out;
   int layers, blocks, most, R;
 };

@@ -330,10 +330,10 @@ k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T, i
   return device_status(launch_tree_attention(a, stream), fn);
 }
 
-k3_status k3_kv_commit(const k3_kv_cache *cache, int layers, int64_t layer_stride, const int32_t *table, int blocks,
-                       const int32_t *ctx, const int32_t *accepted, const int32_t *n_accepted, int most, int R,
-                       int32_t *ctx_out, k3_stream_t stream) {
-  const char *fn = "k3_kv_commit";
+static k3_status commit(const char *fn, const k3_kv_cache *cache, int layers, int64_t layer_stride,
+                        const int32_t *table, int blocks, const int32_t *ctx, const int32_t *kv_lens,
+                        const int32_t *accepted, const int32_t *n_accepted, int most, int R, int32_t *ctx_out,
+                        k3_stream_t stream) {
   if (k3_status s = check_cache(fn, cache)) return s;
   if (k3_status s = check_table(fn, R, blocks, cache->page_size)) return s;
   KV_NEED(layers >= 1 && layers <= 65535, "%s: layers=%d outside [1, 65535]", fn, layers);
@@ -345,13 +345,14 @@ k3_status k3_kv_commit(const k3_kv_cache *cache, int layers, int64_t layer_strid
   KV_PTR(accepted, 4);
   KV_PTR(n_accepted, 4);
   KV_PTR(ctx_out, 4);
-  KV_NEED(ctx_out != ctx && ctx_out != n_accepted && ctx_out != accepted, "%s: ctx_out is the same array as an input",
-          fn);
+  KV_NEED(ctx_out != ctx && ctx_out != kv_lens && ctx_out != n_accepted && ctx_out != accepted,
+          "%s: ctx_out is the same array as an input", fn);
   KvCommitArgs a = {};
   a.c = *cache;
   a.layer_stride = layer_stride;
   a.table = table;
   a.ctx = ctx;
+  a.kv_lens = kv_lens;
   a.accepted = accepted;
   a.n_accepted = n_accepted;
   a.ctx_out = ctx_out;
@@ -360,6 +361,22 @@ k3_status k3_kv_commit(const k3_kv_cache *cache, int layers, int64_t layer_strid
   a.most = most;
   a.R = R;
   return device_status(launch_kv_commit(a, stream), fn);
+}
+
+k3_status k3_kv_commit(const k3_kv_cache *cache, int layers, int64_t layer_stride, const int32_t *table, int blocks,
+                       const int32_t *ctx, const int32_t *accepted, const int32_t *n_accepted, int most, int R,
+                       int32_t *ctx_out, k3_stream_t stream) {
+  return commit("k3_kv_commit", cache, layers, layer_stride, table, blocks, ctx, nullptr, accepted, n_accepted, most,
+                R, ctx_out, stream);
+}
+
+k3_status k3_kv_commit_ex(const k3_kv_cache *cache, int layers, int64_t layer_stride, const int32_t *table, int blocks,
+                          const int32_t *ctx, const int32_t *kv_lens, const int32_t *accepted,
+                          const int32_t *n_accepted, int most, int R, int32_t *ctx_out, k3_stream_t stream) {
+  const char *fn = "k3_kv_commit_ex";
+  KV_PTR(kv_lens, 4);
+  return commit(fn, cache, layers, layer_stride, table, blocks, ctx, kv_lens, accepted, n_accepted, most, R, ctx_out,
+                stream);
 }
 
 }  // extern "C"

@@ -1,6 +1,9 @@
 // Commit of the accepted paths: rows of keys and values move down within a
 // request's pages, in every layer.
 //
+// A table keeps the ids of pages that a request has given back, and they may
+// be another's by then; kv_lens says how far a step's places are its own.
+//
 // One workgroup per request and layer; each thread owns one 16-byte column of
 // a row (heads x keys and values) and takes it through the path's rows, eight
 // rows in flight. accepted ascends strictly, so accepted[i] >= i: a row that
@@ -33,6 +36,7 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(KvCommitArgs 
   __shared__ int bad;
   const int r = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;
   const int n = a.n_accepted[r], ctx = a.ctx[r];
+  const int len = a.kv_lens ? a.kv_lens[r] : INT32_MAX;
   const int es = a.c.dtype == K3_E4M3 ? 1 : 2;
   const int32_t *row = a.table + (size_t)r * a.blocks, *acc = a.accepted + (size_t)r * a.most;
   if (tid == 0) bad = n < 0 || n > a.most || ctx < 0;
@@ -42,7 +46,9 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(KvCommitArgs 
   for (int i = tid; i < todo; i += kCommitThreads) {
     const int from = acc[i], before = i ? acc[i - 1] : -1;
     int64_t s_at = -1, d_at = -1;
-    if (from > before) {  // before >= -1: ascending, and not below zero
+    // before >= -1: ascending, and not below zero; then i <= from, so that one
+    // look at the request's places is enough
+    if (from > before && (int64_t)ctx + from < len) {
       s_at = place_offset(a, row, (int64_t)ctx + from, es);
       d_at = from == i ? s_at : place_offset(a, row, (int64_t)ctx + i, es);
     }
