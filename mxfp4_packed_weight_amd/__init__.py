@@ -527,14 +527,50 @@ def k3_moe_layer_from_logits_cached(X, logits, bias, cache, n_experts, hidden, i
 
 
 # ---- paged key/value cache --------------------------------------------------
-# Tensors only (strides and types are read off them); a cache is the handle
-# that k3_kv_cache_of returns, made once per layer.
+# Tensors only: strides are read off the rows' tensors, and what the C calls
+# cannot see is checked here: types, dense arrays, and that they hold as much
+# as the call's sizes say. A cache is the handle that k3_kv_cache_of returns,
+# made once per layer.
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
 _kv_codes = {}
+_int32 = _float32 = None  # torch's, once an array was given
+
+
+def _array(name, t, dtype, n):
+    """Address of a dense array of at least n values."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: a dense array of at least {n} values, not {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _ints(name, t, n):
+    """The same of int32 (None: NULL)."""
+    global _int32
+    if t is None:
+        return None
+    if t.dtype is _int32 and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    import torch
+    _int32 = torch.int32
+    return _array(name, t, _int32, n)
+
+
+def _floats(name, t, n):
+    """The same of float32 (None: NULL)."""
+    global _float32
+    if t is None:
+        return None
+    if _float32 is None:
+        import torch
+        _float32 = torch.float32
+    return _array(name, t, _float32, n)
 
 
 def _kv_dtype(t):
@@ -548,16 +584,19 @@ def _kv_dtype(t):
     return code
 
 
-def _heads(name, t, dtype, D):
-    """Token stride of rows [T, heads, D] or [T, heads * D] with dense heads."""
-    if _kv_dtype(t) != dtype:
+def _heads(name, t, dtype, T, heads, D):
+    """Token stride of rows [T, heads, D] or [T, heads * D] with dense heads,
+    the first of as many tokens and heads or more."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, not the type of the call's other rows")
     shape, strides = t.shape, t.stride()
-    dense = len(shape) in (2, 3) and strides[-1] == 1
-    if dense and len(shape) == 3:
-        dense = shape[2] == D and (shape[1] == 1 or strides[1] == D)
-    if not dense:
-        raise ValueError(f"{name}: rows [T, heads, {D}] with dense heads, "
+    if len(shape) == 2:
+        dense = shape[1] >= heads * D
+    else:
+        dense = (len(shape) == 3 and shape[1] >= heads and shape[2] == D
+                 and (shape[1] == 1 or strides[1] == D))
+    if not dense or strides[-1] != 1 or shape[0] < T:
+        raise ValueError(f"{name}: rows [{T}, {heads}, {D}] with dense heads, "
                          f"not {tuple(shape)} with strides {strides}")
     return strides[0]
 
@@ -584,23 +623,24 @@ def k3_kv_cache_of(k, v, k_scale=None, v_scale=None):
 def k3_kv_plan(ctx, new, parents, R, T, n_pages, page_size, blocks, held, ring, ring_state, table,
                held_out, ring_out, cu, kv_lens, slots, positions, mask, words, status,
                stream=None):
-    _call("k3_kv_plan", _ptr(ctx), _ptr(new), _ptr(parents), R, T, n_pages, page_size, blocks,
-          _ptr(held), _ptr(ring), _ptr(ring_state), _ptr(table), _ptr(held_out), _ptr(ring_out),
-          _ptr(cu), _ptr(kv_lens), _ptr(slots), _ptr(positions), _ptr(mask), words, _ptr(status),
-          _stream(stream))
+    _call("k3_kv_plan", _ints("ctx", ctx, R), _ints("new", new, R), _ints("parents", parents, T), R,
+          T, n_pages, page_size, blocks, _ints("held", held, R), _ints("ring", ring, n_pages),
+          _ints("ring_state", ring_state, 2), _ints("table", table, R * blocks),
+          _ints("held_out", held_out, R), _ints("ring_out", ring_out, 2), _ints("cu", cu, R + 1),
+          _ints("kv_lens", kv_lens, R), _ints("slots", slots, T), _ints("positions", positions, T),
+          _ints("mask", mask, 0 if parents is None else T * words), words,
+          _ints("status", status, 2), _stream(stream))
 
 
 def k3_qk_norm_rope(q_in, k_in, v_in, T, Hq, wq, wk, eps, inv_freq, rot, interleaved, positions,
                     q_out, cache, slots, stream=None):
-    dt, D = _kv_dtype(q_in), cache.head_dim
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w.dtype != q_in.dtype:
-            raise TypeError(f"{name} is {w.dtype}, not the type of the call's rows")
-    _call("k3_qk_norm_rope", _ptr(q_in), _heads("q_in", q_in, dt, D), _ptr(k_in),
-          _heads("k_in", k_in, dt, D), _ptr(v_in), _heads("v_in", v_in, dt, D), dt, T, Hq,
-          _ptr(wq), _ptr(wk), eps, _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(positions),
-          _ptr(q_out), _heads("q_out", q_out, dt, D), ctypes.byref(cache), _ptr(slots),
-          _stream(stream))
+    code, dt, H, D = _kv_dtype(q_in), q_in.dtype, cache.n_heads, cache.head_dim
+    wq, wk = _array("wq", wq, dt, D), _array("wk", wk, dt, D)
+    _call("k3_qk_norm_rope", q_in.data_ptr(), _heads("q_in", q_in, dt, T, Hq, D), k_in.data_ptr(),
+          _heads("k_in", k_in, dt, T, H, D), v_in.data_ptr(), _heads("v_in", v_in, dt, T, H, D), code, T,
+          Hq, wq, wk, eps, _floats("inv_freq", inv_freq, rot // 2), rot, int(bool(interleaved)),
+          _ints("positions", positions, T), q_out.data_ptr(), _heads("q_out", q_out, dt, T, Hq, D),
+          ctypes.byref(cache), _ints("slots", slots, T), _stream(stream))
 
 
 def k3_tree_attention_workspace_bytes(T, Hq, n_heads, head_dim):
@@ -609,20 +649,27 @@ def k3_tree_attention_workspace_bytes(T, Hq, n_heads, head_dim):
 
 def k3_tree_attention(q, T, Hq, cache, table, blocks, cu, kv_lens, R, mask, words, scale, out, ws,
                       lse=None, stream=None):
-    dt, D = _kv_dtype(q), cache.head_dim
-    _call("k3_tree_attention", _ptr(q), _heads("q", q, dt, D), dt, T, Hq, ctypes.byref(cache),
-          _ptr(table), blocks, _ptr(cu), _ptr(kv_lens), R, _ptr(mask), words, scale, _ptr(out),
-          _heads("out", out, dt, D), _ptr(ws), _nbytes(ws), _ptr(lse), _stream(stream))
+    code, dt, D = _kv_dtype(q), q.dtype, cache.head_dim
+    q_stride, out_stride = _heads("q", q, dt, T, Hq, D), _heads("out", out, dt, T, Hq, D)
+    if not ws.is_contiguous():
+        raise ValueError(f"ws: dense bytes, not {tuple(ws.shape)} with strides {ws.stride()}")
+    _call("k3_tree_attention", q.data_ptr(), q_stride, code, T, Hq, ctypes.byref(cache),
+          _ints("table", table, R * blocks), blocks, _ints("cu", cu, R + 1),
+          _ints("kv_lens", kv_lens, R), R, _ints("mask", mask, T * words), words, scale, out.data_ptr(),
+          out_stride, ws.data_ptr(), _nbytes(ws), _floats("lse", lse, T * Hq), _stream(stream))
 
 
 def k3_kv_commit(cache, layers, layer_stride, table, blocks, ctx, accepted, n_accepted, most, R,
                  ctx_out, stream=None):
-    _call("k3_kv_commit", ctypes.byref(cache), layers, layer_stride, _ptr(table), blocks,
-          _ptr(ctx), _ptr(accepted), _ptr(n_accepted), most, R, _ptr(ctx_out), _stream(stream))
+    _call("k3_kv_commit", ctypes.byref(cache), layers, layer_stride,
+          _ints("table", table, R * blocks), blocks, _ints("ctx", ctx, R),
+          _ints("accepted", accepted, R * most), _ints("n_accepted", n_accepted, R), most, R,
+          _ints("ctx_out", ctx_out, R), _stream(stream))
 
 
 def k3_kv_commit_ex(cache, layers, layer_stride, table, blocks, ctx, kv_lens, accepted, n_accepted, most,
                     R, ctx_out, stream=None):
-    _call("k3_kv_commit_ex", ctypes.byref(cache), layers, layer_stride, _ptr(table), blocks,
-          _ptr(ctx), _ptr(kv_lens), _ptr(accepted), _ptr(n_accepted), most, R, _ptr(ctx_out),
-          _stream(stream))
+    _call("k3_kv_commit_ex", ctypes.byref(cache), layers, layer_stride,
+          _ints("table", table, R * blocks), blocks, _ints("ctx", ctx, R),
+          _ints("kv_lens", kv_lens, R), _ints("accepted", accepted, R * most),
+          _ints("n_accepted", n_accepted, R), most, R, _ints("ctx_out", ctx_out, R), _stream(stream))
