@@ -669,7 +669,8 @@ k3_status k3_kv_plan(const int32_t *ctx, const int32_t *new_, const int32_t *par
  * leave either). fp32 throughout, angles in fp64, one rounding at the end.
  * q_in [T][Hq][D], k_in and v_in [T][n_heads][D] with token strides in
  * elements (multiples of 8) and dense heads, q_out likewise; dtype K3_BF16 or
- * K3_F16 for all of them and wq, wk [D]. The cache holds dtype or e4m3.
+ * K3_F16 for all of them and wq, wk [D]. The cache holds dtype or e4m3. q_out
+ * may be q_in, with its stride; otherwise it is apart from the inputs.
  * inv_freq fp32 [rot / 2]; rot a multiple of 16, 0 <= rot <= D (0: no
  * rotation, inv_freq may be NULL). */
 k3_status k3_qk_norm_rope(const void *q_in, int64_t q_stride, const void *k_in,

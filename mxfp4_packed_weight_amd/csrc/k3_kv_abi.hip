@@ -228,6 +228,8 @@ k3_status k3_qk_norm_rope(const void *q_in, int64_t q_stride, const void *k_in, 
   if (k3_status s = check_rows(fn, "v_stride", v_stride, T, cache->n_heads, D)) return s;
   if (k3_status s = check_rows(fn, "q_out_stride", q_out_stride, T, Hq, D)) return s;
   KV_NEED(q_out != k_in && q_out != v_in, "%s: q_out is k_in or v_in", fn);
+  KV_NEED(q_out != q_in || T == 1 || q_out_stride == q_stride, "%s: q_out is q_in, with q_out_stride=%lld for q_stride=%lld",
+          fn, (long long)q_out_stride, (long long)q_stride);
   QkArgs a = {};
   a.q = (const uint16_t *)q_in;
   a.k = (const uint16_t *)k_in;

@@ -1,12 +1,13 @@
-"""Refusals of the commit with the step's lengths, before any launch (no GPU
-needed): the addresses given are never touched."""
+"""Refusals of the commit with the step's lengths, and of queries in place at
+another stride, before any launch (no GPU needed): the addresses given are
+never touched."""
 import ctypes
 import os
 
 import pytest
 
 import mxfp4_packed_weight_amd as K
-from tests.test_kv_host import COMMIT, _cache, _p
+from tests.test_kv_host import COMMIT, QK, _cache, _p
 
 
 @pytest.fixture(scope="module")
@@ -28,3 +29,12 @@ def test_commit_ex_refusals(L, change, status, says):
     a = {**COMMIT, "lens": _p(9), **change, "cache": ctypes.byref(_cache())}
     assert L.k3_kv_commit_ex(*(a[k] for k in ORDER)) == status
     assert says in K.last_error() and "k3_kv_commit_ex" in K.last_error()
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(out=_p(3), os=66 * 128), 2), (dict(out=_p(3), qs=66 * 128), 2), (dict(out=_p(3), T=0, os=66 * 128), 0)])
+def test_queries_in_place_keep_their_stride(L, change, status):
+    """Rows written at another stride would land on rows that are still to be read."""
+    a = {**QK, **change, "cache": ctypes.byref(_cache())}
+    assert L.k3_qk_norm_rope(*a.values()) == status
+    assert status == 0 or "q_out is q_in" in K.last_error()
