@@ -627,9 +627,9 @@ typedef struct k3_kv_cache {
  * missing pages, with those of the requests before it, are more than the free
  * ones is not served: it keeps what it holds, kv_lens[r] = 0 and its slots
  * are -1. So is one with a length that is negative or past the table's row,
- * held[r] outside [0, blocks], more nodes than the mask has bits, or more
- * pages to give back than the ring has room for (it asks for none and gives
- * none). `table` and `ring` are updated in place;
+ * held[r] outside [0, blocks], more nodes than the mask has bits (these ask
+ * for no pages and give none), or whose pages to give back, with those of the
+ * requests before it, are more than the ring has room for. `table` and `ring` are updated in place;
  * the others are outputs apart from the inputs:
  * A row of the table keeps the ids of pages given back, past held_out[r];
  * they are no longer the request's, and may be another's.
@@ -666,7 +666,8 @@ k3_status k3_kv_plan(const int32_t *ctx, const int32_t *new_, const int32_t *par
  * or 2i and 2i + 1 if `interleaved`. Rotated queries go to q_out; rotated
  * keys and the values as they are go to the cache rows at slots[t] (rows with
  * a slot outside [0, n_pages * P) are not written; two tokens with one slot
- * leave either). fp32 throughout, angles in fp64, one rounding at the end.
+ * leave values of either in it). fp32 throughout, angles in fp64, one
+ * rounding at the end.
  * q_in [T][Hq][D], k_in and v_in [T][n_heads][D] with token strides in
  * elements (multiples of 8) and dense heads, q_out likewise; dtype K3_BF16 or
  * K3_F16 for all of them and wq, wk [D]. The cache holds dtype or e4m3. q_out
@@ -696,7 +697,8 @@ k3_status k3_qk_norm_rope(const void *q_in, int64_t q_stride, const void *k_in,
  * q and out [T][Hq][D] of dtype K3_BF16 or K3_F16 with token strides
  * in elements (multiples of 8); the cache holds dtype or e4m3. Scores, the
  * softmax's maximum and sum and the output's sum are fp32; the weights are
- * rounded to dtype for the product with the values. Results do not depend on
+ * rounded to dtype for the product with the values, their sum is of the
+ * unrounded ones. bf16 values beyond 2^119 may overflow in the output's sum. Results do not depend on
  * timing: the same call gives the same bits. Needs a workspace of
  * k3_tree_attention_workspace_bytes(T, Hq, n_heads, head_dim) bytes (0 for
  * shapes it does not support). */

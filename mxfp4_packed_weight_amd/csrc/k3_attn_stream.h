@@ -22,9 +22,10 @@
 // The rows' places come from the page table one run ahead, through a few
 // hundred bytes of LDS per wave.
 //
-// Measured: one token of each of 64 requests of up to 8191 places, 8 key heads
-// of 128 in bf16, 1.09 GB: 188 us, 5.7 TB/s (a copy on this card moves 5.0, a
-// plain read up to 7.0); in e4m3 109 us.
+// Measured: one token of each of 64 requests of up to 8191 places, 8 query heads
+// to a key head, 8 key heads of 128 in bf16, 1.09 GB: 188 us, 5.8 TB/s (a plain
+// read on this card reaches 7.1, a copy 5.1); in e4m3 108 us, 5.1 TB/s. 8 key
+// heads of 64: 103 us, 5.3 TB/s; 4 of 256: 188 us, 5.8 TB/s.
 #pragma once
 
 #include "k3_attn.h"

@@ -16,14 +16,30 @@ hipError_t launch_attn_f16(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_f16_e4m3(const AttnArgs &a, hipStream_t s);
 
 // Rows per tile: up to 32 rows of an average request (16 at a head of 256) go
-// to the streaming kernel, more to the tiled kernel. Streaming against tiled,
-// 32 requests of 8192 places, us:
-//   rows             16          32          48
-//   128, bf16     175 / 197   177 / 197   343 / 198
-//   128, e4m3     100 / 140   119 / 141   239 / 156
-//    64, bf16      95 / 104   103 / 104   197 / 107
-//   256, bf16     196 / 205   318 / 207   563 / 212
-// and 63 requests of one token with one of 512, 8 rows to a node: 381 / 224.
+// to the streaming kernel, more to the tiled kernel. Streaming (its better
+// tile) against tiled, 32 requests of 8192 places, 8 query heads to a key head,
+// us:
+//   rows                           16          32          48
+//   8 key heads of 128, bf16    174 / 193   177 / 193   340 / 194
+//   8 of 128, e4m3               99 / 138   119 / 138   223 / 150
+//   8 of 64, bf16                95 / 105   104 / 105   198 / 106
+//   4 of 256, bf16              178 / 203   307 / 205   501 / 209
+//   8 of 256, bf16              335 / 366   659 / 366   984 / 368
+// The lengths are on the device, so the average is all that the rule sees, and
+// R counts requests without tokens too. A batch of unlike requests can
+// therefore be slower than with the other kernel, since each streaming tile of
+// a long request reads all of its keys again. 8 key heads of 128, ragged
+// contexts of up to 8191, streaming as the rule's tile has it / tiled:
+//   255 tokens, one chunk of 512, 8 heads to a key head, bf16   1373 / 785
+//   the same, e4m3                                              1160 / 818
+//   255 tokens, one chunk of 255, bf16                           934 / 775
+//   255 tokens, one chunk of 255, e4m3                           614 / 759
+//   255 tokens, one tree of 64, bf16                             802 / 783
+//   63 tokens, one chunk of 512, bf16 (the rule: tiled)          654 / 277
+// and 16 key heads, a head each, one chunk of 2048 among 256 requests of which
+// the others have no tokens: 168 / 51 over no context, 1230 / 164 over 8192.
+// A caller that knows its batch puts the long requests last and makes two
+// calls, of the first requests' tokens alone and of the last requests.
 int attn_tile_rows(int T, int G, int R, int D) {
   const long long rows = ((long long)T * G + R - 1) / R;
   if (rows <= 16) return 16;

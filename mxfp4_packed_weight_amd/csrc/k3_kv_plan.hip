@@ -12,7 +12,9 @@
 // The time is that of a launch and of three dependent reads (lengths; table
 // or ring; parents): 4.2 us for 16 requests of one token, 8.3 us for 1024
 // requests with trees of up to 64 nodes (10.4 where the same workgroups had
-// pages and tokens).
+// pages and tokens). Masks of more than 64 nodes are kept in memory, a
+// dependent read and write for each ancestor: 16 trees of 64 nodes 8.7 us, of
+// 65 10.5, of 256 39, of 1024 237; 4 chains of 1024 nodes 731.
 #include "k3_kv.h"
 
 namespace k3 {

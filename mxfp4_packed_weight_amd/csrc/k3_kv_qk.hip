@@ -14,7 +14,11 @@
 //
 // Bytes bound it: each row is read and written once, and the arithmetic
 // (about 80 instructions a pass) hides under that. 16384 tokens of 64 query and
-// 8 key heads of 128, 671 MB: 142 us, 4.7 TB/s (a copy: 5.0).
+// 8 key heads of 128, 671 MB: 142 us, 4.7 TB/s (a copy: 5.0). Few tokens are
+// bound by latency: slot and position, then the frequencies (the branch on
+// `turns` has each of a lane's four or eight loads waited for by itself), the
+// weights and the rows follow one another. 1000 tokens over an e4m3 cache, 19
+// MB: 8.4 us, of which 3.9 are the bytes'.
 #include "k3_kv.h"
 
 namespace k3 {
