@@ -89,3 +89,27 @@ def test_whole_error_over_long_rows(ctx, new, H, G, D, dt, cache, P, trees):
     s = kv.attn_case(ctx, new, H, G, D, dt, cache, P, D + sum(new), trees=trees)
     got, _ = kv.run_attn(s)
     say(f"  {N.check(got, N.exact(s), s):.3f} half steps")
+
+
+@pytest.mark.parametrize("D,dt,cache", [(128, "bf16", "bf16"), (64, "f16", "e4m3")])
+@pytest.mark.parametrize("ctx,new,first", [([40, 700, 5, 300, 90], [1, 1, 1, 1, 130], 4),
+                                           ([0] * 30 + [500], [0] * 30 + [90], 30),
+                                           ([9, 100, 2000], [2, 33, 60], 1)])
+def test_one_batch_in_two_calls(D, dt, cache, ctx, new, first):
+    """The first requests with their own tokens, then the others by the rest
+    of the arrays: what one call gives, to the reference's bound."""
+    import torch
+    import mxfp4_packed_weight_amd as K
+    from tests import _kv as R_
+    say(f"two calls D={D} {dt} {cache} new={new}")
+    s = kv.attn_case(ctx, new, 2, 8, D, dt, cache, 16, 11, trees=False)
+    T, Hq, _ = s["q"].shape
+    out, lse = torch.full_like(s["q"], 7.0), torch.full((T, Hq), 7.0, device="cuda")
+    ws = torch.empty(K.k3_tree_attention_workspace_bytes(T, Hq, 2, D), dtype=torch.uint8, device="cuda")
+    c, blocks = K.k3_kv_cache_of(s["kc"], s["vc"], s["ks"], s["vs"]), s["table"].shape[1]
+    table, cu, lens = R_.i32(s["table"]), R_.i32(s["cu"]), R_.i32(s["lens"])
+    K.k3_tree_attention(s["q"], int(s["cu"][first]), Hq, c, table, blocks, cu, lens, first, None, 1, s["scale"], out,
+                        ws, lse=lse)
+    K.k3_tree_attention(s["q"], T, Hq, c, table[first:], blocks, cu[first:], lens[first:], len(new) - first, None, 1,
+                        s["scale"], out, ws, lse=lse)
+    R_.check_attention(out, lse, kv.reference(s), dt, int(max(s["lens"])))
