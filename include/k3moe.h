@@ -605,6 +605,7 @@ k3_status k3_moe_layer_cached(const uint16_t *x, const uint16_t *router_w,
 #define K3_BF16 0
 #define K3_F16 1
 #define K3_E4M3 2
+#define K3_F32 3
 #define K3_MAX_REQUESTS 4096
 #define K3_MAX_TREE_WORDS 32
 #define K3_MAX_ACCEPTED 1024
@@ -735,6 +736,60 @@ k3_status k3_kv_commit_ex(const k3_kv_cache *cache, int layers, int64_t layer_st
                           const int32_t *kv_lens, const int32_t *accepted,
                           const int32_t *n_accepted, int most, int R,
                           int32_t *ctx_out, k3_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The rest of a step: the norm between the halves of a layer, and what is
+ * said about the tokens at its end. Checks, alignment and T = 0 as for the
+ * cache calls above.
+ * ---------------------------------------------------------------------- */
+
+/* The residual's addition and the norm: s = x + residual (residual NULL: x),
+ * y = s * rsqrt(mean(s^2) + eps) * w over rows of `hidden` values, in fp32
+ * throughout; the norm is of the unrounded s. Rows of dtype K3_BF16 or
+ * K3_F16 with strides in elements (multiples of 8); hidden a multiple of 8,
+ * <= K3_MAX_HIDDEN; w [hidden] of dtype. Outputs, each rounded once:
+ *   sum     s (may be NULL)
+ *   y       y (may be NULL if y8 is given)
+ *   y8      e4m3 codes of y / scale (may be NULL; 8-byte aligned, its stride
+ *           a multiple of 8), with
+ *   scales  fp32 [T][hidden / group], dense: max |y| / 448 over each `group`
+ *           consecutive values; group is hidden (a scale per row), or 32, 64,
+ *           128, 256 or 512 and divides it. A scale below 2^-126 is written
+ *           as 0, with codes of 0. A group with a value that is not finite
+ *           has a scale that is not finite.
+ * sum and y may be x or residual with that input's stride; otherwise the
+ * outputs are apart from the inputs and from each other. Rows whose mean
+ * square is past fp32's range give 0 (and NaN where s is infinite). */
+k3_status k3_add_rms_norm(const void *x, int64_t x_stride, const void *residual,
+                          int64_t residual_stride, int dtype, int T, int hidden,
+                          const void *w, float eps, void *sum, int64_t sum_stride,
+                          void *y, int64_t y_stride, uint8_t *y8,
+                          int64_t y8_stride, float *scales, int group,
+                          k3_stream_t stream);
+
+/* Log probabilities under p = softmax(beta * logits) for each of T rows of V
+ * logits (dtype K3_BF16, K3_F16 or K3_F32; stride in elements, any from V
+ * on; aligned to their own size). beta is the inverse temperature, in
+ * [2^-20, 2^20]. Outputs, fp32 [T] unless said:
+ *   logprob      log p of tokens[t] (int32 [T]; both NULL: not wanted); a
+ *                token outside [0, V) (a padded row) has -inf
+ *   entropy      - sum p log p (may be NULL)
+ *   lse          log sum exp(beta * logits) (may be NULL)
+ *   top, top_logprob  int32 and fp32 [T][k]: the k largest logits' indices
+ *                and log p, in descending order, equal ones in the order of
+ *                their indices; 0 <= k <= min(K3_MAX_TOPK, V)
+ * A logit of -inf has p = 0, and is listed after all others; in a row of
+ * nothing else every log p and lse are -inf, the entropy 0. A row with NaN or
+ * +inf has NaN for all three; NaN logits are not listed, and places left over
+ * have index -1 and NaN. Sums and differences are fp32. ws: at least
+ * k3_token_logprobs_workspace_bytes(T, V, k) bytes (NULL if that is 0). The
+ * same call gives the same bits. */
+size_t k3_token_logprobs_workspace_bytes(int T, int V, int k);
+k3_status k3_token_logprobs(const void *logits, int64_t stride, int dtype, int T,
+                            int V, float beta, const int32_t *tokens, int k,
+                            float *logprob, float *entropy, float *lse,
+                            int32_t *top, float *top_logprob, void *ws,
+                            size_t ws_bytes, k3_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -22,7 +22,7 @@ _functions = {}  # those called so far
 K3_OK, K3_ERR_ARG, K3_ERR_CONFIG, K3_ERR_MEMORY, K3_ERR_DEVICE = 0, 1, 2, 3, 4
 K3_MAX_EXPERTS, K3_MAX_TOPK, K3_MAX_SHARED = 4096, 64, 8
 K3_WAIT_LIMIT_DEFAULT = 1 << 20
-K3_BF16, K3_F16, K3_E4M3 = 0, 1, 2
+K3_BF16, K3_F16, K3_E4M3, K3_F32 = 0, 1, 2, 3
 K3_MAX_REQUESTS, K3_MAX_TREE_WORDS, K3_MAX_ACCEPTED, K3_MAX_HEADS = 4096, 32, 1024, 1024
 
 # (name, restype, argtypes) of every exported symbol in include/k3moe.h
@@ -122,6 +122,10 @@ SIGNATURES = [
                                ctypes.c_float, _vp, _i64, _vp, _sz, _vp, _vp]),
     ("k3_kv_commit", _i, [_vp, _i, _i64, _vp, _i, _vp, _vp, _vp, _i, _i, _vp, _vp]),
     ("k3_kv_commit_ex", _i, [_vp, _i, _i64, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp]),
+    ("k3_add_rms_norm", _i, [_vp, _i64, _vp, _i64, _i, _i, _i, _vp, ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _i64,
+                             _vp, _i, _vp]),
+    ("k3_token_logprobs_workspace_bytes", _sz, [_i, _i, _i]),
+    ("k3_token_logprobs", _i, [_vp, _i64, _i, _i, _i, ctypes.c_float, _vp, _i] + [_vp] * 6 + [_sz, _vp]),
 ]
 
 
@@ -673,3 +677,44 @@ def k3_kv_commit_ex(cache, layers, layer_stride, table, blocks, ctx, kv_lens, ac
           _ints("table", table, R * blocks), blocks, _ints("ctx", ctx, R),
           _ints("kv_lens", kv_lens, R), _ints("accepted", accepted, R * most),
           _ints("n_accepted", n_accepted, R), most, R, _ints("ctx_out", ctx_out, R), _stream(stream))
+
+
+# ---- the rest of a step -------------------------------------------------------
+
+def _rows(name, t, dtype, T, n):
+    """Address and stride of rows [T, n], the first of as many or more (None: NULL)."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < T or shape[1] < n or strides[1] != 1:
+        raise ValueError(f"{name}: dense rows [{T}, {n}], not {tuple(shape)} with strides {strides}")
+    return t.data_ptr(), strides[0]
+
+
+def k3_add_rms_norm(x, residual, T, hidden, w, eps, sum_out=None, y=None, y8=None, scales=None, group=0,
+                    stream=None):
+    import torch
+    code, dt = _kv_dtype(x), x.dtype
+    _call("k3_add_rms_norm", *_rows("x", x, dt, T, hidden), *_rows("residual", residual, dt, T, hidden), code, T,
+          hidden, _array("w", w, dt, hidden), eps, *_rows("sum_out", sum_out, dt, T, hidden),
+          *_rows("y", y, dt, T, hidden), *_rows("y8", y8, torch.float8_e4m3fn, T, hidden),
+          _floats("scales", scales, T * hidden // group if group > 0 else 0), group, _stream(stream))
+
+
+def k3_token_logprobs_workspace_bytes(T, V, k):
+    return lib().k3_token_logprobs_workspace_bytes(T, V, k)
+
+
+def k3_token_logprobs(logits, T, V, beta, tokens, k, logprob, entropy, lse, top, top_logprob, ws, stream=None):
+    import torch
+    dt = logits.dtype
+    code = K3_F32 if dt is torch.float32 else _kv_dtype(logits)
+    address, stride = _rows("logits", logits, dt, T, V)
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError(f"ws: dense bytes, not {tuple(ws.shape)} with strides {ws.stride()}")
+    _call("k3_token_logprobs", address, stride, code, T, V, beta, _ints("tokens", tokens, T), k,
+          _floats("logprob", logprob, T), _floats("entropy", entropy, T), _floats("lse", lse, T),
+          _ints("top", top, T * k), _floats("top_logprob", top_logprob, T * k), _ptr(ws),
+          0 if ws is None else _nbytes(ws), _stream(stream))

@@ -1,12 +1,11 @@
 // C ABI of the paged key/value cache: argument checks and launches. As in
 // k3_abi.hip every check happens before the first launch.
 #include <math.h>
-#include <stdarg.h>
-#include <stdio.h>
 
 #include <algorithm>
 
 #include "k3_attn.h"
+#include "k3_check.h"
 
 namespace k3 {
 
@@ -71,37 +70,6 @@ hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t s) {
   return f8 ? launch_attn_f16_e4m3(a, s) : launch_attn_f16(a, s);
 }
 
-namespace {
-
-constexpr int kMaxTokens = 1 << 20;
-
-k3_status refuse(k3_status s, const char *fmt, ...) {
-  char text[400];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(text, sizeof text, fmt, ap);
-  va_end(ap);
-  set_error("%s", text);
-  return s;
-}
-
-#define KV_PTR(p, align)                                                                       \
-  do {                                                                                         \
-    if (!(p)) return refuse(K3_ERR_ARG, "%s: %s is NULL", fn, #p);                             \
-    if ((uintptr_t)(p) % (align))                                                              \
-      return refuse(K3_ERR_ARG, "%s: %s is not %d-byte aligned", fn, #p, (int)(align));        \
-  } while (0)
-// A pointer that may be NULL.
-#define KV_OPT(p, align)                                                                       \
-  do {                                                                                         \
-    if ((uintptr_t)(p) % (align))                                                              \
-      return refuse(K3_ERR_ARG, "%s: %s is not %d-byte aligned", fn, #p, (int)(align));        \
-  } while (0)
-#define KV_NEED(cond, ...)                                     \
-  do {                                                         \
-    if (!(cond)) return refuse(K3_ERR_CONFIG, __VA_ARGS__);    \
-  } while (0)
-
 k3_status check_cache(const char *fn, const k3_kv_cache *c) {
   if (!c) return refuse(K3_ERR_ARG, "%s: cache is NULL", fn);
   KV_PTR(c->k, 16);
@@ -148,8 +116,6 @@ k3_status check_table(const char *fn, int R, int blocks, int page_size) {
           "%s: blocks=%d, page_size=%d: at least one block, at most 2^30 places", fn, blocks, page_size);
   return K3_OK;
 }
-
-}  // namespace
 
 }  // namespace k3
 

@@ -1,0 +1,127 @@
+// The residual's addition and the root-mean-square norm, in 16 bits and in e4m3
+// with scales.
+//
+//   s = x + residual,  y = s r w,  r = rsqrt(mean s^2 + eps)
+//   scale = max |y| / 448 over a group,  code = e4m3(y / scale)
+// A workgroup takes a row, and each thread keeps eight values of up to eight
+// stretches of it in registers: a row is read once. The largest |y| of a group
+// is r times the largest |s w|, so that the row's sum of squares and a scale per
+// row need one exchange between the waves, and a group of up to 512 values is
+// in neighbouring lanes of a wave. The sum goes into the norm unrounded.
+#include "k3_rows.h"
+#include "k3_step.h"
+
+namespace k3 {
+
+namespace {
+
+constexpr int kNormThreads = 1024, kNormWaves = kNormThreads / 64;
+
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float larger(float a, float b) { return a > b || a != a ? a : b; }
+
+template <bool BF, bool QUANT, int VEC>
+__global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) {
+  __shared__ float sums[kNormWaves], tops[kNormWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int64_t t = blockIdx.x;
+  const int vectors = a.hidden / 8;
+  float h[VEC][8], hw[VEC][8];
+  uint4 xs[VEC], rs[VEC], ws[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; i++) {
+    const int v = i * blockDim.x + threadIdx.x;
+    xs[i] = rs[i] = ws[i] = uint4{0, 0, 0, 0};
+    if (v < vectors) {
+      xs[i] = *(const uint4 *)(a.x + t * a.x_stride + 8 * v);
+      if (a.residual) rs[i] = *(const uint4 *)(a.residual + t * a.residual_stride + 8 * v);
+      ws[i] = *(const uint4 *)(a.w + 8 * v);
+    }
+  }
+  float ss = 0.f, top[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; i++) {
+    const int v = i * blockDim.x + threadIdx.x;
+    float r[8], w[8];
+    unpack8<BF>(xs[i], h[i]);
+    unpack8<BF>(rs[i], r);
+    unpack8<BF>(ws[i], w);
+    top[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      h[i][j] += r[j];
+      ss = fmaf(h[i][j], h[i][j], ss);
+      hw[i][j] = h[i][j] * w[j];
+      if (QUANT) top[i] = larger(fabsf(hw[i][j]), top[i]);
+    }
+    if (a.sum && v < vectors) *(uint4 *)(a.sum + t * a.sum_stride + 8 * v) = pack8<BF>(h[i]);
+  }
+  const bool per_row = QUANT && a.group == a.hidden;
+  float most = 0.f;
+  if (per_row) {
+#pragma unroll
+    for (int i = 0; i < VEC; i++) most = larger(top[i], most);
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) {
+    ss += __shfl_xor(ss, m);
+    if (per_row) most = larger(most, __shfl_xor(most, m));
+  }
+  if (lane == 0) {
+    sums[wave] = ss;
+    tops[wave] = most;
+  }
+  __syncthreads();
+  ss = sums[0];
+  most = tops[0];
+  for (int i = 1; i < waves; i++) {
+    ss += sums[i];
+    most = larger(most, tops[i]);
+  }
+  const float r = rsqrtf(ss / (float)a.hidden + a.eps);
+  const int lanes = per_row ? 64 : a.group / 8;  // of a group
+#pragma unroll
+  for (int i = 0; i < VEC; i++) {
+    const int v = i * blockDim.x + threadIdx.x;
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) y[j] = hw[i][j] * r;
+    if (a.y && v < vectors) *(uint4 *)(a.y + t * a.y_stride + 8 * v) = pack8<BF>(y);
+    if (QUANT) {
+      float largest = per_row ? most : top[i];
+      if (!per_row)
+        for (int m = 1; m < lanes; m *= 2) largest = larger(largest, __shfl_xor(largest, m));
+      if (v >= vectors) continue;
+      float scale = largest * r * (1.f / 448.f);
+      if (scale < 0x1p-126f) scale = 0.f;  // (not for NaN)
+      const float up = scale == 0.f ? 0.f : 1.f / scale;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const float q = y[j] * up;
+        y[j] = q != q ? q : fminf(fmaxf(q, -448.f), 448.f);
+      }
+      *(uint2 *)(a.y8 + t * a.y8_stride + 8 * v) = to_e4m3(y);
+      if (per_row ? v == 0 : v % lanes == 0) a.scales[t * (a.hidden / a.group) + v * 8 / a.group] = scale;
+    }
+  }
+}
+
+template <bool BF, bool QUANT>
+hipError_t by_vectors(const NormArgs &a, hipStream_t s) {
+  const int vectors = a.hidden / 8;
+  auto threads = [&](int vec) { return ((vectors + vec - 1) / vec + 63) / 64 * 64; };
+  // One row has its latency alone: a vector to a thread. Many: two.
+  const int vec = vectors <= kNormThreads && a.T < num_cus() ? 1 : 2;
+  if (vec == 1) add_rms_norm_kernel<BF, QUANT, 1><<<a.T, threads(1), 0, s>>>(a);
+  else add_rms_norm_kernel<BF, QUANT, 2><<<a.T, threads(2), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_add_rms_norm(const NormArgs &a, hipStream_t s) {
+  if (a.dtype == K3_BF16) return a.y8 ? by_vectors<true, true>(a, s) : by_vectors<true, false>(a, s);
+  return a.y8 ? by_vectors<false, true>(a, s) : by_vectors<false, false>(a, s);
+}
+
+}  // namespace k3
