@@ -737,6 +737,59 @@ k3_status k3_kv_commit_ex(const k3_kv_cache *cache, int layers, int64_t layer_st
                           const int32_t *n_accepted, int most, int R,
                           int32_t *ctx_out, k3_stream_t stream);
 
+/* Attention with a sliding window: k3_tree_attention, but of the places that
+ * a row sees there only those below `sinks` (the first tokens stay visible)
+ * and those above x - window for the row's position x, itself included. x is
+ * L - n + i or, with a mask, L - n + (set bits among the row's first n) - 1,
+ * its depth in the tree; window >= 32 * words then, so that a node sees all
+ * of its ancestors. window = 0: no window (and no sinks); both <= 2^30. The
+ * places left out are not read. Same workspace. */
+k3_status k3_window_attention(const void *q, int64_t q_stride, int dtype, int T,
+                              int Hq, const k3_kv_cache *cache, const int32_t *table,
+                              int blocks, const int32_t *cu, const int32_t *kv_lens,
+                              int R, const int32_t *mask, int words, int window,
+                              int sinks, float scale, void *out, int64_t out_stride,
+                              void *ws, size_t ws_bytes, float *lse,
+                              k3_stream_t stream);
+
+/* A cache in 8 bits with a scale for each page and head: an e4m3 cache (its
+ * k_scale and v_scale NULL, page_size a multiple of 4) and two dense arrays of
+ * exponent bytes [n_pages][n_heads], k_exp and v_exp: a code in a page
+ * stands for itself times 2^(byte - 127). Bytes are in [1, 254]; pages that
+ * hold nothing yet need none.
+ *
+ * k3_kv_append appends a step's rows: token cu[r] + i of request r goes to
+ * the place kv_lens[r] - n + i, n = cu[r + 1] - cu[r]. A page's exponent for
+ * a head becomes the smallest 2^e with max |x| <= 448 2^e over the new rows
+ * that go there (1 if all are 0), or stays where the page holds earlier rows
+ * (places below kv_lens[r] - n) whose exponent is larger; if it rises, those
+ * rows' codes are rounded to the new one (only codes that leave e4m3's normal
+ * range lose anything). Rows are rounded once, to nearest even. NaN stays
+ * NaN; infinities do not count for the exponent and become +-448 2^e; fp16
+ * values stop at +-61440, so that fp16 has them again. k_in, v_in as in
+ * k3_qk_norm_rope (keys rotated), dtype K3_BF16 or K3_F16. A request whose cu
+ * is not ascending within [0, T], or whose kv_lens is below n or past the
+ * table's row, is left out (with cu out of order others may be left out, too);
+ * so are pages outside [0, n_pages). The pages that a call appends to are
+ * their request's own.
+ *
+ * k3_block_attention is k3_window_attention without a mask over such a
+ * cache: window = 0 for all places. Codes times their powers are exact in
+ * bf16; in fp16 to 2^-25, and below 65520. k3_kv_commit moves codes without
+ * their exponents: it is not for these caches. */
+k3_status k3_kv_append(const void *k_in, int64_t k_stride, const void *v_in,
+                       int64_t v_stride, int dtype, int T, const k3_kv_cache *cache,
+                       uint8_t *k_exp, uint8_t *v_exp, const int32_t *table,
+                       int blocks, const int32_t *cu, const int32_t *kv_lens, int R,
+                       k3_stream_t stream);
+k3_status k3_block_attention(const void *q, int64_t q_stride, int dtype, int T,
+                             int Hq, const k3_kv_cache *cache, const uint8_t *k_exp,
+                             const uint8_t *v_exp, const int32_t *table, int blocks,
+                             const int32_t *cu, const int32_t *kv_lens, int R,
+                             int window, int sinks, float scale, void *out,
+                             int64_t out_stride, void *ws, size_t ws_bytes,
+                             float *lse, k3_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * The rest of a step: the norm between the halves of a layer, and what is
  * said about the tokens at its end. Checks, alignment and T = 0 as for the

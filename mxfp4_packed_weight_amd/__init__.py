@@ -122,6 +122,11 @@ SIGNATURES = [
                                ctypes.c_float, _vp, _i64, _vp, _sz, _vp, _vp]),
     ("k3_kv_commit", _i, [_vp, _i, _i64, _vp, _i, _vp, _vp, _vp, _i, _i, _vp, _vp]),
     ("k3_kv_commit_ex", _i, [_vp, _i, _i64, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp]),
+    ("k3_window_attention", _i, [_vp, _i64, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _i,
+                                 ctypes.c_float, _vp, _i64, _vp, _sz, _vp, _vp]),
+    ("k3_kv_append", _i, [_vp, _i64, _vp, _i64, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _vp]),
+    ("k3_block_attention", _i, [_vp, _i64, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i,
+                                ctypes.c_float, _vp, _i64, _vp, _sz, _vp, _vp]),
     ("k3_add_rms_norm", _i, [_vp, _i64, _vp, _i64, _i, _i, _i, _vp, ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _i64,
                              _vp, _i, _vp]),
     ("k3_token_logprobs_workspace_bytes", _sz, [_i, _i, _i]),
@@ -679,6 +684,52 @@ def k3_kv_commit_ex(cache, layers, layer_stride, table, blocks, ctx, kv_lens, ac
           _ints("n_accepted", n_accepted, R), most, R, _ints("ctx_out", ctx_out, R), _stream(stream))
 
 
+def k3_window_attention(q, T, Hq, cache, table, blocks, cu, kv_lens, R, mask, words, window, sinks, scale, out, ws,
+                        lse=None, stream=None):
+    code, dt, D = _kv_dtype(q), q.dtype, cache.head_dim
+    q_stride, out_stride = _heads("q", q, dt, T, Hq, D), _heads("out", out, dt, T, Hq, D)
+    _dense("ws", ws)
+    _call("k3_window_attention", q.data_ptr(), q_stride, code, T, Hq, ctypes.byref(cache),
+          _ints("table", table, R * blocks), blocks, _ints("cu", cu, R + 1), _ints("kv_lens", kv_lens, R), R,
+          _ints("mask", mask, T * words), words, window, sinks, scale, out.data_ptr(), out_stride, ws.data_ptr(),
+          _nbytes(ws), _floats("lse", lse, T * Hq), _stream(stream))
+
+
+def _dense(name, t):
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: dense bytes, not {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _exponents(name, t, cache):
+    """Address of the exponent bytes [pages, heads] of a cache's pages."""
+    import torch
+    if t.dtype is not torch.uint8:
+        raise TypeError(f"{name} is {t.dtype}, not torch.uint8")
+    if not t.is_contiguous() or t.numel() < cache.n_pages * cache.n_heads:
+        raise ValueError(f"{name}: dense bytes [{cache.n_pages}, {cache.n_heads}], not {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def k3_kv_append(k_in, v_in, T, cache, k_exp, v_exp, table, blocks, cu, kv_lens, R, stream=None):
+    code, dt, H, D = _kv_dtype(k_in), k_in.dtype, cache.n_heads, cache.head_dim
+    _call("k3_kv_append", k_in.data_ptr(), _heads("k_in", k_in, dt, T, H, D), v_in.data_ptr(),
+          _heads("v_in", v_in, dt, T, H, D), code, T, ctypes.byref(cache), _exponents("k_exp", k_exp, cache),
+          _exponents("v_exp", v_exp, cache), _ints("table", table, R * blocks), blocks, _ints("cu", cu, R + 1),
+          _ints("kv_lens", kv_lens, R), R, _stream(stream))
+
+
+def k3_block_attention(q, T, Hq, cache, k_exp, v_exp, table, blocks, cu, kv_lens, R, window, sinks, scale, out, ws,
+                       lse=None, stream=None):
+    code, dt, D = _kv_dtype(q), q.dtype, cache.head_dim
+    q_stride, out_stride = _heads("q", q, dt, T, Hq, D), _heads("out", out, dt, T, Hq, D)
+    _dense("ws", ws)
+    _call("k3_block_attention", q.data_ptr(), q_stride, code, T, Hq, ctypes.byref(cache),
+          _exponents("k_exp", k_exp, cache), _exponents("v_exp", v_exp, cache), _ints("table", table, R * blocks),
+          blocks, _ints("cu", cu, R + 1), _ints("kv_lens", kv_lens, R), R, window, sinks, scale, out.data_ptr(),
+          out_stride, ws.data_ptr(), _nbytes(ws), _floats("lse", lse, T * Hq), _stream(stream))
+
+
 # ---- the rest of a step -------------------------------------------------------
 
 def _rows(name, t, dtype, T, n):
@@ -712,8 +763,8 @@ def k3_token_logprobs(logits, T, V, beta, tokens, k, logprob, entropy, lse, top,
     dt = logits.dtype
     code = K3_F32 if dt is torch.float32 else _kv_dtype(logits)
     address, stride = _rows("logits", logits, dt, T, V)
-    if ws is not None and not ws.is_contiguous():
-        raise ValueError(f"ws: dense bytes, not {tuple(ws.shape)} with strides {ws.stride()}")
+    if ws is not None:
+        _dense("ws", ws)
     _call("k3_token_logprobs", address, stride, code, T, V, beta, _ints("tokens", tokens, T), k,
           _floats("logprob", logprob, T), _floats("entropy", entropy, T), _floats("lse", lse, T),
           _ints("top", top, T * k), _floats("top_logprob", top_logprob, T * k), _ptr(ws),

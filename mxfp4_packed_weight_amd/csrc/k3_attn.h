@@ -14,6 +14,11 @@
 // line's order. The lengths are on the device, so every workgroup works the
 // line out for itself: one prefix sum over the requests, and a closed form
 // within each.
+//
+// Windows. A row at position x sees the places below `sinks` and those above
+// x - window. Of a tile's places only the blocks up to the sinks' end and from
+// its first row's window on are taken: they are numbered without the gap, and
+// real_place() turns such a place into the cache's.
 #pragma once
 
 #include <math.h>
@@ -78,10 +83,12 @@ __device__ __forceinline__ int node_of(const AttnArgs &a, int row) {
 // fixed, the first tile's places, what each next one has more. The last one's
 // places count for less if it is of up to HALF rows. T * Hq <= 2^30 rows and
 // 2^30 places keep all sums below 2^61.
-template <int RT, int HALF>
+// With a window a tile has at most `cap`: tiles from `capped` on.
+template <int RT, int HALF, bool WIN>
 struct Cost {
   int tiles, last_rows;
   long long base, slope, all;
+  long long cap, capped;  // WIN
   static constexpr long long kFixed = 16 * kFixedPlaces<RT>;
   __device__ __forceinline__ Cost(const AttnArgs &a, const Request &q) {
     const long long rows = (long long)q.n * a.G;
@@ -90,14 +97,27 @@ struct Cost {
     const bool causal = !a.mask && q.len >= q.n;
     slope = causal ? a.slope : 0;
     base = 16ll * (causal ? q.len - q.n : q.len) + slope;
+    if constexpr (WIN) {
+      cap = 16ll * a.sinks + 16ll * a.window + (causal ? slope : 16ll * q.n);
+      // (off by a tile or so it would do as well: every workgroup has the same)
+      const double room = (double)(cap - base);
+      capped = room < 0. ? 0 : !slope ? tiles : min((long long)(room * __builtin_amdgcn_rcp((double)slope)) + 1, (long long)tiles);
+    }
     all = tiles ? of_first(tiles - 1) + of(tiles - 1) : 0;
   }
   // a place's cost; the first x tiles of a key head; tile x
   __device__ __forceinline__ int weight(int x) const { return x == tiles - 1 && last_rows <= HALF ? kHalfCost : 16; }
   __device__ __forceinline__ long long of_first(long long x) const {
+    if constexpr (WIN) {
+      const long long y = min(x, capped);
+      return x * kFixed + y * base + slope * (y * (y - 1) / 2) + (x - y) * cap;
+    }
     return x * (kFixed + base) + slope * (x * (x - 1) / 2);
   }
-  __device__ __forceinline__ long long of(int x) const { return kFixed + ((base + slope * x) * weight(x) >> 4); }
+  __device__ __forceinline__ long long of(int x) const {
+    const long long places = WIN && x >= capped ? cap : base + slope * x;
+    return kFixed + (places * weight(x) >> 4);
+  }
   __device__ __forceinline__ long long of_request(const AttnArgs &a) const { return all * a.c.n_heads; }
 };
 
@@ -112,13 +132,13 @@ struct Line {
 template <int THREADS>
 __device__ __forceinline__ int run_of(int R) { return (R + THREADS - 1) / THREADS; }
 
-template <int RT, int HALF, int THREADS>
+template <int RT, int HALF, bool WIN, int THREADS>
 __device__ __forceinline__ void line_of_tiles(const AttnArgs &a, Line<THREADS> &L) {
   const int tid = threadIdx.x, lane = tid & 63, per = run_of<THREADS>(a.R);
   long long own = 0;
   for (int r = tid * per; r < min(a.R, tid * per + per); r++) {
     const Request q = request_of(a, r);
-    own += Cost<RT, HALF>(a, q).of_request(a);
+    own += Cost<RT, HALF, WIN>(a, q).of_request(a);
     L.request[tid] = q;
   }
   long long incl = own;
@@ -160,10 +180,18 @@ struct Tile {
   int weight;              // Cost::weight
   long long first, after;  // its stretch of the line
   int tiles;               // of its key head
+  // WIN: blocks of the sinks, blocks that are left out behind them, the first
+  // place that is in the window of all rows
+  int sink_blocks, skipped, near;
 };
+// Place y of a tile's, counted without the gap, in the cache.
+template <bool WIN, int KB>
+__device__ __forceinline__ int real_place(const Tile &t, int y) {
+  return WIN && y >= t.sink_blocks * KB ? y + t.skipped * KB : y;
+}
 // The rest of a tile from q, r, h, x and first.
-template <int RT, int KB, int HALF>
-__device__ __forceinline__ void fill_tile(const AttnArgs &a, Tile &t, const Cost<RT, HALF> &cost) {
+template <int RT, int KB, int HALF, bool WIN>
+__device__ __forceinline__ void fill_tile(const AttnArgs &a, Tile &t, const Cost<RT, HALF, WIN> &cost) {
   t.tiles = cost.tiles;
   t.row0 = t.x * RT;
   t.rows = t.x == cost.tiles - 1 ? cost.last_rows : RT;
@@ -172,9 +200,17 @@ __device__ __forceinline__ void fill_tile(const AttnArgs &a, Tile &t, const Cost
   t.places = t.q.len;
   if (!a.mask) t.places = min(t.q.len, max(0, t.q.len - t.q.n + node_of(a, t.row0 + t.rows - 1) + 1));
   t.blocks = t.places > 0 ? (t.places - 1) / KB + 1 : 1;
+  if constexpr (WIN) {
+    // (a tree's row is at its request's last committed place or later)
+    const int ctx = t.q.len - t.q.n, first = a.mask ? ctx - 1 : ctx + node_of(a, t.row0);
+    t.near = t.places - a.window;
+    t.sink_blocks = (min(a.sinks, max(t.places, 0)) + KB - 1) / KB;
+    t.skipped = max(0, min(max(0, first - a.window + 1) / KB, t.blocks - 1) - t.sink_blocks);
+    t.blocks -= t.skipped;
+  }
 }
 // The tile that place u of the line is in.
-template <int RT, int KB, int HALF, int THREADS>
+template <int RT, int KB, int HALF, bool WIN, int THREADS>
 __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &L, long long u) {
   Tile t;
   // the last thread whose requests begin at or before it, and its request
@@ -189,12 +225,12 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &
   t.r = run * per;
   t.q = request_again(a, L, t.r);
   for (; t.r + 1 < min(a.R, run * per + per); t.r++) {
-    const long long all = Cost<RT, HALF>(a, t.q).of_request(a);
+    const long long all = Cost<RT, HALF, WIN>(a, t.q).of_request(a);
     if (before + all > u) break;
     before += all;
     t.q = request_again(a, L, t.r + 1);
   }
-  const Cost<RT, HALF> cost(a, t.q);
+  const Cost<RT, HALF, WIN> cost(a, t.q);
   // (the product is off by less than 1: n_heads <= 2^10)
   t.h = (int)((double)(u - before) * __builtin_amdgcn_rcp((double)cost.all));
   t.h = min(max(t.h, 0), a.c.n_heads - 1);
@@ -209,11 +245,11 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &
   }
   t.x = lo;
   t.first = head + cost.of_first(lo);
-  fill_tile<RT, KB, HALF>(a, t, cost);
+  fill_tile<RT, KB, HALF, WIN>(a, t, cost);
   return t;
 }
 // The next tile (there is one).
-template <int RT, int KB, int HALF, int THREADS>
+template <int RT, int KB, int HALF, bool WIN, int THREADS>
 __device__ __forceinline__ void next_tile(const AttnArgs &a, const Line<THREADS> &L, Tile &t) {
   t.first = t.after;
   if (++t.x == t.tiles) {
@@ -224,7 +260,7 @@ __device__ __forceinline__ void next_tile(const AttnArgs &a, const Line<THREADS>
       while (t.q.n == 0 && t.r + 1 < a.R);
     }
   }
-  fill_tile<RT, KB, HALF>(a, t, Cost<RT, HALF>(a, t.q));
+  fill_tile<RT, KB, HALF, WIN>(a, t, Cost<RT, HALF, WIN>(a, t.q));
 }
 
 // The tile's first block that is done after place u of the line (any rising
@@ -278,18 +314,18 @@ __device__ __forceinline__ JoinJob *join_jobs(const AttnArgs &a, int B) {
 
 // The walk of a workgroup over its stretch of the line, with
 // segment(tile, first block, block after the last, slot or -1).
-template <int RT, int KB, int HALF, int D, int THREADS, class Segment>
+template <int RT, int KB, int HALF, bool WIN, int D, int THREADS, class Segment>
 __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
   __shared__ Line<THREADS> L;
-  line_of_tiles<RT, HALF, THREADS>(a, L);
+  line_of_tiles<RT, HALF, WIN, THREADS>(a, L);
   const int B = gridDim.x, b = place_in_line(blockIdx.x, B);
   const Stretches line(a, in_all_lanes(L.pre[THREADS]));
   const long long begin = line.begin(b), end = line.begin(b + 1);
   JoinJob job = {0, 0, 0, 0, -1, -1, -1, 0};
   Tile tile;
   for (long long u = begin; u < end;) {
-    if (u == begin) tile = tile_at<RT, KB, HALF>(a, L, u);
-    else next_tile<RT, KB, HALF>(a, L, tile);
+    if (u == begin) tile = tile_at<RT, KB, HALF, WIN>(a, L, u);
+    else next_tile<RT, KB, HALF, WIN>(a, L, tile);
     const int lo = block_from<RT, KB>(tile, u), hi = block_from<RT, KB>(tile, end);
     const int slot = lo == hi || (lo == 0 && hi == tile.blocks) ? -1 : lo ? 2 * b : 2 * b + 1;
     if (u > tile.first) job.head_slot = slot;
@@ -327,12 +363,15 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   if (BF) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
-// Two e4m3 values (exact in either 16-bit type): bytes 0, 1 or 2, 3 of w.
+// Two e4m3 values (exact in either 16-bit type): bytes 0, 1 or 2, 3 of w,
+// times a power of two.
 template <bool BF, bool HI>
-__device__ __forceinline__ uint32_t widen2(uint32_t w) {
-  if (BF) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, HI));
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, HI));
+__device__ __forceinline__ uint32_t widen2(uint32_t w, float power = 1.f) {
+  if (BF) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, power, HI));
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, power, HI));
 }
+// 2^(byte - 127)
+__device__ __forceinline__ float power_of(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
 template <bool BF>
 __device__ __forceinline__ f32x4 mfma16(u32x4 x, u32x4 y, f32x4 c) {
   if (BF)
@@ -410,6 +449,26 @@ __device__ __forceinline__ uint32_t seen(const AttnArgs &a, const Request &q, in
   const uint32_t lo = word_of(a, q, i, w);
   if (!sh) return lo & present;
   return ((lo >> sh) | (word_of(a, q, i, w + 1) << (32 - sh))) & present;
+}
+
+// The first place in the window of node i (its position is its request's last
+// committed place's and the nodes of its own that it sees further on).
+__device__ __forceinline__ int window_of(const AttnArgs &a, const Request &q, int i) {
+  int at = q.len - q.n + i;
+  if (a.mask) {
+    at = q.len - q.n - 1;
+    const uint32_t *row = (const uint32_t *)a.mask + (size_t)(q.t0 + i) * a.words;
+    for (int w = 0; w < a.words && 32 * w < q.n; w++) {
+      const int left = q.n - 32 * w;
+      at += __popc(left < 32 ? row[w] & ((1u << left) - 1) : row[w]);
+    }
+  }
+  return at - a.window + 1;
+}
+// Of the 32 places from k0 on, those in a window from `near` on or below the sinks' end.
+__device__ __forceinline__ uint32_t in_window(const AttnArgs &a, int near, int k0) {
+  const int y = near - k0, z = a.sinks - k0;
+  return (y <= 0 ? 0xffffffffu : y < 32 ? ~0u << y : 0u) | (z >= 32 ? 0xffffffffu : z > 0 ? (1u << z) - 1 : 0u);
 }
 
 }  // namespace k3

@@ -3,6 +3,6 @@
 
 namespace k3 {
 
-hipError_t launch_attn_f16(const AttnArgs &a, hipStream_t s) { return attn_by_dim<false, false>(a, s); }
+hipError_t launch_attn_f16(const AttnArgs &a, hipStream_t s) { return attn_by_dim<false, false, kAllPlaces>(a, s); }
 
 }  // namespace k3

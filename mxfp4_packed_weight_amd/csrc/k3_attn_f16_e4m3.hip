@@ -3,6 +3,6 @@
 
 namespace k3 {
 
-hipError_t launch_attn_f16_e4m3(const AttnArgs &a, hipStream_t s) { return attn_by_dim<false, true>(a, s); }
+hipError_t launch_attn_f16_e4m3(const AttnArgs &a, hipStream_t s) { return attn_by_dim<false, true, kAllPlaces>(a, s); }
 
 }  // namespace k3

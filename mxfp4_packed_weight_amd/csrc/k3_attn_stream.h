@@ -40,8 +40,9 @@ template <bool F8, int D>
 constexpr int kStreamRuns = F8 && D <= 128 ? 2 : 1;
 
 // BF: bf16 (else fp16) queries, outputs and weights; F8: the cache is e4m3.
-template <bool BF, bool F8, int D, int QT>
+template <bool BF, bool F8, int D, int QT, int MODE>
 struct Stream {
+  static constexpr bool WIN = MODE != kAllPlaces, BLK = MODE == kBlocks;
   static constexpr int RT = 16 * QT, NS = D / 32, DPL = D / 16;
   static constexpr int ES = F8 ? 1 : 2;
   static constexpr int RUNS = kStreamRuns<F8, D>, PLACES = 32 * RUNS;
@@ -53,6 +54,7 @@ struct Stream {
     int64_t offset[kStreamWaves][PLACES];
     float ml[kStreamWaves][2][RT];
     float o[kStreamWaves][16 * kPad];
+    float power[kStreamWaves][2][BLK ? PLACES : 1];  // of the places' keys and values
   };
 
   struct Wave {
@@ -62,6 +64,7 @@ struct Stream {
     f32x4 o[QT][DPL];
     float ref[QT], sum[QT];  // the reference exponent, this lane's part of the sum
     uint32_t present[RUNS];
+    uint32_t k_exp, v_exp;  // BLK: of the lane's place
   };
 
   // Value d of the head that element j of step s holds in lane group g.
@@ -77,7 +80,7 @@ struct Stream {
 
   // The places from k0 on: this lane's (lane % PLACES) page is `page`. Leaves
   // the rows' offsets in LDS; places that are not there read row 0.
-  static __device__ __forceinline__ void places(const AttnArgs &a, Wave &w, int64_t *offset, int lane, int k0,
+  static __device__ __forceinline__ void places(const AttnArgs &a, Wave &w, int64_t *offset, int lane, int h, int k0,
                                                 int page) {
     const int p = k0 + lane % PLACES;
     const bool there = page >= 0 && page < a.c.n_pages;
@@ -89,6 +92,11 @@ struct Stream {
     const uint64_t all = __ballot(there);
 #pragma unroll
     for (int r = 0; r < RUNS; r++) w.present[r] = (uint32_t)(all >> (32 * r));
+    if constexpr (BLK) {  // (on their way before the rows are)
+      const size_t e = (size_t)page * a.c.n_heads + h;
+      w.k_exp = there ? a.k_exp[e] : 127u;  // (0 times a page of nobody's infinity would be none)
+      w.v_exp = there ? a.v_exp[e] : 127u;
+    }
   }
 
   // Keys and values are read once, so they pass the caches by (not kept there
@@ -156,17 +164,18 @@ struct Stream {
     for (int r = 0; r < RUNS; r++) load_v(w, v, offset, r, c, g);
   }
 
-  static __device__ __forceinline__ u32x4 k_operand(const uint32_t (&k)[2][NS][KW], int u, int s) {
+  static __device__ __forceinline__ u32x4 k_operand(const uint32_t (&k)[2][NS][KW], int u, int s, float power) {
     if constexpr (F8)
-      return u32x4{widen2<BF, false>(k[u][s][0]), widen2<BF, true>(k[u][s][0]), widen2<BF, false>(k[u][s][1]),
-                   widen2<BF, true>(k[u][s][1])};
+      return u32x4{widen2<BF, false>(k[u][s][0], power), widen2<BF, true>(k[u][s][0], power),
+                   widen2<BF, false>(k[u][s][1], power), widen2<BF, true>(k[u][s][1], power)};
     else
       return u32x4{k[u][s][0], k[u][s][1], k[u][s][2], k[u][s][3]};
   }
 
-  // V^T operands of the values 4 / ES that word i of the lane's row parts hold.
+  // V^T operands of the values 4 / ES that word i of the lane's row parts hold;
+  // power: of the lane's places 0..3, 4..7 (four are in one page).
   template <class F>
-  static __device__ __forceinline__ void v_operands(const uint32_t (&v)[8][VW], int i, F &&use) {
+  static __device__ __forceinline__ void v_operands(const uint32_t (&v)[8][VW], int i, const float *power, F &&use) {
     if constexpr (F8) {
       uint32_t t[4][2];  // [value][places 0..3, 4..7] as four bytes
 #pragma unroll
@@ -181,8 +190,8 @@ struct Stream {
       }
 #pragma unroll
       for (int e = 0; e < 4; e++)
-        use(4 * i + e, u32x4{widen2<BF, false>(t[e][0]), widen2<BF, true>(t[e][0]), widen2<BF, false>(t[e][1]),
-                             widen2<BF, true>(t[e][1])});
+        use(4 * i + e, u32x4{widen2<BF, false>(t[e][0], power[0]), widen2<BF, true>(t[e][0], power[0]),
+                             widen2<BF, false>(t[e][1], power[1]), widen2<BF, true>(t[e][1], power[1])});
     } else {
       u32x4 lo, hi;
 #pragma unroll
@@ -241,9 +250,19 @@ struct Stream {
 
   // One run of 32 places: scores, weights, and the weighted values.
   template <int RUN>
-  static __device__ __forceinline__ void run(const AttnArgs &a, Wave &w, const Request &rq, const int *node, int k0,
-                                             float scale, const char *v, const int64_t *offset, float *scratch, int c,
-                                             int g) {
+  static __device__ __forceinline__ void run(const AttnArgs &a, Wave &w, const Tile &tile, const int *node,
+                                             const int *near, int k0, float scale, const char *v,
+                                             const int64_t *offset, const float (*power)[BLK ? PLACES : 1],
+                                             float *scratch, int c, int g) {
+    const Request &rq = tile.q;
+    float k_power[2] = {1.f, 1.f}, v_power[2] = {1.f, 1.f};
+    if constexpr (BLK) {
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        k_power[u] = power[0][32 * RUN + 16 * u + c];
+        v_power[u] = power[1][32 * RUN + 16 * u + 4 * g];
+      }
+    }
     f32x4 s[QT][2];
 #pragma unroll
     for (int t = 0; t < QT; t++)
@@ -253,12 +272,14 @@ struct Stream {
     for (int i = 0; i < NS; i++)
 #pragma unroll
       for (int u = 0; u < 2; u++) {
-        const u32x4 k = k_operand(w.k[RUN], u, i);
+        const u32x4 k = k_operand(w.k[RUN], u, i, k_power[u]);
 #pragma unroll
         for (int t = 0; t < QT; t++) s[t][u] = mfma16<BF>(k, w.q[t][i], s[t][u]);
       }
     const uint32_t present = w.present[RUN];
-    const bool drafts = k0 + 32 > rq.len - rq.n, partial = drafts || present != 0xffffffffu;
+    // places that some rows may not see
+    const bool drafts = k0 + 32 > rq.len - rq.n || (WIN && k0 < tile.near && k0 + 32 > a.sinks);
+    const bool partial = drafts || present != 0xffffffffu;
     bool odd = false;
     if (partial) {
       if (present != 0xffffffffu) {
@@ -290,6 +311,7 @@ struct Stream {
       uint32_t vis = 0xffffffffu;
       if (partial) {
         vis = drafts ? seen(a, rq, node[t], k0, present) : present;
+        if (WIN && drafts) vis &= in_window(a, near[t], k0);
 #pragma unroll
         for (int j = 0; j < 8; j++)
           if (!((vis >> (16 * (j / 4) + 4 * g + j % 4)) & 1)) x[j] = -INFINITY;
@@ -320,7 +342,7 @@ struct Stream {
     }
 #pragma unroll
     for (int i = 0; i < VW; i++)
-      v_operands(w.v[RUN], i, [&](int e, u32x4 operand) {
+      v_operands(w.v[RUN], i, v_power, [&](int e, u32x4 operand) {
 #pragma unroll
         for (int t = 0; t < QT; t++) w.o[t][e] = mfma16<BF>(operand, p[t], w.o[t][e]);
       });
@@ -333,13 +355,14 @@ struct Stream {
     const Request &rq = tile.q;
     const int rows = rq.n * a.G;
     Wave w;
-    int node[QT];
+    int node[QT], near[QT];
 #pragma unroll
     for (int t = 0; t < QT; t++) {
       const int row = tile.row0 + 16 * t + c;
       const bool on = row < rows;
       const int i = on ? node_of(a, row) : 0, hq = tile.h * a.G + (on ? row - i * a.G : 0);
       node[t] = i;
+      near[t] = WIN ? window_of(a, rq, i) : 0;
       const uint16_t *q = a.q + (rq.t0 + i) * a.q_stride + hq * D;
 #pragma unroll
       for (int s = 0; s < NS; s++) w.q[t][s] = on ? *(const u32x4 *)(q + d_of(s, g)) : u32x4{0, 0, 0, 0};
@@ -353,20 +376,29 @@ struct Stream {
     const char *v = (const char *)a.c.v + tile.h * a.c.head_stride * ES;
     const int32_t *table = a.table + (size_t)tile.r * a.blocks;
     int64_t *offset = L.offset[wave];
-    const int end = (int)min((long long)hi * KB, (long long)tile.places);
+    const int end = (int)min((long long)hi * KB, (long long)tile.places - (WIN ? tile.skipped * KB : 0));
+    auto real = [&](int y) { return real_place<WIN, KB>(tile, y); };  // (a wave's places are in one block)
     int k0 = lo * KB + PLACES * wave;
-    int page = table_entry(a, table, k0 + lane % PLACES, rq.len);
+    int page = table_entry(a, table, real(k0) + lane % PLACES, rq.len);
     if (k0 < end) {
-      places(a, w, offset, lane, k0, page);
+      places(a, w, offset, lane, tile.h, real(k0), page);
       load(w, k, v, offset, c, g);
-      page = table_entry(a, table, k0 + KB + lane % PLACES, rq.len);
+      page = table_entry(a, table, real(k0 + KB) + lane % PLACES, rq.len);
       for (; k0 < end; k0 += KB) {
-        run<0>(a, w, rq, node, k0, scale, v, offset, L.o[wave], c, g);
+        if constexpr (BLK) {
+          if (lane < PLACES) {
+            L.power[wave][0][lane] = power_of(w.k_exp);
+            L.power[wave][1][lane] = power_of(w.v_exp);
+          }
+          wave_sync();
+        }
+        run<0>(a, w, tile, node, near, real(k0), scale, v, offset, L.power[wave], L.o[wave], c, g);
         if (RUNS > 1 && k0 + 32 < end)
-          run<RUNS - 1>(a, w, rq, node, k0 + 32, scale, v, offset + PLACES - 32, L.o[wave], c, g);
+          run<RUNS - 1>(a, w, tile, node, near, real(k0) + 32, scale, v, offset + PLACES - 32, L.power[wave],
+                        L.o[wave], c, g);
         if (k0 + KB < end) {
-          places(a, w, offset, lane, k0 + KB, page);
-          page = table_entry(a, table, k0 + 2 * KB + lane % PLACES, rq.len);
+          places(a, w, offset, lane, tile.h, real(k0 + KB), page);
+          page = table_entry(a, table, real(k0 + 2 * KB) + lane % PLACES, rq.len);
           load(w, k, v, offset, c, g);
         }
       }
@@ -439,11 +471,15 @@ struct Stream {
   }
 };
 
-template <bool BF, bool F8, int D, int QT>
-__global__ __launch_bounds__(kStreamThreads) void attn_stream_kernel(AttnArgs a) {
-  using S = Stream<BF, F8, D, QT>;
+// Waves that are to fit on a SIMD (the variants with a window need telling).
+template <int D, int QT, int MODE>
+constexpr int kStreamFit = MODE != kAllPlaces && 64 * QT * D <= 64 * 128 ? 2 : 1;
+
+template <bool BF, bool F8, int D, int QT, int MODE>
+__global__ __launch_bounds__(kStreamThreads, (kStreamFit<D, QT, MODE>)) void attn_stream_kernel(AttnArgs a) {
+  using S = Stream<BF, F8, D, QT, MODE>;
   __shared__ typename S::Lds L;
-  walk<S::RT, S::KB, 0, D, kStreamThreads>(a, [&](const Tile &tile, int lo, int hi, int slot) {
+  walk<S::RT, S::KB, 0, S::WIN, D, kStreamThreads>(a, [&](const Tile &tile, int lo, int hi, int slot) {
     S::segment(a, L, tile, lo, hi, slot, gridDim.x);
   });
 }

@@ -68,8 +68,9 @@ constexpr int kAttnKeys = D == 256 ? 32 : 64;
 template <int D>
 constexpr int kPairedRows = D == 256 ? 0 : 128;
 
-template <bool BF, bool F8, int D>
+template <bool BF, bool F8, int D, int MODE>
 struct Tiled {
+  static constexpr bool WIN = MODE != kAllPlaces, BLK = MODE == kBlocks;
   static constexpr int NW = kAttnWaves<D>, RT = 32 * NW, KB = kAttnKeys<D>, kThreads = kAttnThreads<D>;
   static constexpr bool kPhases = NW == 8;           // two waves to a SIMD, a phase apart
   static constexpr int NS = D / 16, DT = D / 32;     // steps over the head, tiles of the output
@@ -88,9 +89,10 @@ struct Tiled {
 
   struct Lds {
     alignas(16) char buf[kBuffers * kBuffer + kRaws * kRaw];  // keys of a block, values of the one before
-    int64_t row[kListed * KB];  // where the places' rows are, of kListed blocks in turn
+    int64_t row[kListed * KB];  // where the places' rows are, of kListed blocks in turn (BLK: 48 bits, and two exponents)
     uint32_t present[kListed * KB / 32];  // which places of a block are there
     int odd;                    // values that are not finite were set to zero
+    int near[WIN ? RT : 1];     // where the rows' windows begin (few blocks ask)
   };
 
   template <int KT>
@@ -120,19 +122,29 @@ struct Tiled {
   }
   // Lists half of kListed blocks, from block x on, and says which of them have
   // places that are not there (their rows are read from the cache's first).
-  static __device__ __forceinline__ uint64_t list(const AttnArgs &a, Lds &L, const int32_t *table, int x, int end,
-                                                  uint64_t holes) {
+  static __device__ __forceinline__ uint64_t list(const AttnArgs &a, Lds &L, const Tile &tile, const int32_t *table,
+                                                  int x, int end, uint64_t holes) {
     const int at = x % kListed;
     constexpr int N = kListed / 2 * KB / kThreads;
     int page[N];  // (all loads at once: the table has at least one entry)
 #pragma unroll
     for (int i = 0; i < N; i++)
-      page[i] = table[min(block_of(a, x * KB + i * kThreads + threadIdx.x), (uint32_t)a.blocks - 1)];
+      page[i] = table[min(block_of(a, real_place<WIN, KB>(tile, x * KB + i * kThreads + threadIdx.x)),
+                          (uint32_t)a.blocks - 1)];
+    [[maybe_unused]] uint64_t exps[N];
+    if constexpr (BLK) {
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        const bool there = page[i] >= 0 && page[i] < a.c.n_pages;
+        const size_t e = (size_t)(there ? page[i] : 0) * a.c.n_heads + tile.h;
+        exps[i] = (uint64_t)(a.k_exp[e] | (uint32_t)a.v_exp[e] << 8) << 48;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      const int n = i * kThreads + threadIdx.x, p = x * KB + n;
-      const int64_t row = p < end ? row_of(a, p, block_of(a, p), page[i]) : -1;
-      L.row[at * KB + n] = row < 0 ? 0 : row;
+      const int n = i * kThreads + threadIdx.x, y = x * KB + n, p = real_place<WIN, KB>(tile, y);
+      const int64_t row = y < end ? row_of(a, p, block_of(a, p), page[i]) : -1;
+      L.row[at * KB + n] = row < 0 ? 0 : BLK ? (int64_t)((uint64_t)row | exps[i]) : row;
       const uint64_t there = __ballot(row >= 0);
       if (n % 32 == 0) L.present[at * (KB / 32) + n / 32] = (uint32_t)(there >> (n & 32));
     }
@@ -163,12 +175,13 @@ struct Tiled {
     const int group = NL > 1 ? wave * NR + i : wave % (NW / 2);
     return L.row + x % kListed * KB + group * RPL + lane / CH;
   }
+  static __device__ __forceinline__ int64_t bytes_of(int64_t row) { return BLK ? row & ((1ll << 48) - 1) : row; }
   static __device__ __forceinline__ Rows rows_of(const Lds &L, int x, int lo, uint32_t lane, int wave) {
     Rows r;
 #pragma unroll
     for (int i = 0; i < NR; i++) {
-      r.key[i] = *listed(L, x, i, lane, wave);
-      r.value[i] = *listed(L, max(x - 1, lo), i, lane, wave);
+      r.key[i] = bytes_of(*listed(L, x, i, lane, wave));
+      r.value[i] = bytes_of(*listed(L, max(x - 1, lo), i, lane, wave));
     }
     return r;
   }
@@ -177,7 +190,7 @@ struct Tiled {
     Rows r;
 #pragma unroll
     for (int i = 0; i < NR; i++) {
-      r.key[i] = *listed(L, x, i, lane, wave);
+      r.key[i] = bytes_of(*listed(L, x, i, lane, wave));
       r.value[i] = now.key[i];
     }
     return r;
@@ -196,10 +209,11 @@ struct Tiled {
       copy((values ? v + r.value[i / 2] : k + r.key[i / 2]) + chunk, to + (values ? KB * CH * 16 : 0) + group * 1024);
     }
   }
-  // A block of e4m3 rows from LDS into LDS.
-  static __device__ __forceinline__ void widen(const lds_char *from, lds_char *to) {
-    auto wide = [](uint32_t x, uint32_t y) {
-      return u32x4{widen2<BF, false>(x), widen2<BF, true>(x), widen2<BF, false>(y), widen2<BF, true>(y)};
+  // A turn's e4m3 rows from LDS into LDS: keys of block x, values of block x - 1.
+  static __device__ __forceinline__ void widen(const Lds &L, const lds_char *from, lds_char *to, int b, int lo) {
+    auto wide = [](uint32_t x, uint32_t y, float power) {
+      return u32x4{widen2<BF, false>(x, power), widen2<BF, true>(x, power), widen2<BF, false>(y, power),
+                   widen2<BF, true>(y, power)};
     };
 #pragma unroll
     for (int i = 0; i < kRaw / 16 / kThreads; i++) {
@@ -207,8 +221,13 @@ struct Tiled {
       const int row = x / CH, chunk = 2 * (x % CH);
       const u32x4 w = *(const __attribute__((address_space(3))) u32x4 *)(from + 16 * x);
       const int f = row < KB ? swizzle_k(row) : swizzle_v(row);
-      *(__attribute__((address_space(3))) u32x4 *)(to + row * ROW + 16 * (chunk ^ f)) = wide(w[0], w[1]);
-      *(__attribute__((address_space(3))) u32x4 *)(to + row * ROW + 16 * ((chunk + 1) ^ f)) = wide(w[2], w[3]);
+      float power = 1.f;
+      if constexpr (BLK) {  // (blocks before the first have nothing that is used)
+        const int of = max(row < KB ? b : b - 1, lo);
+        power = power_of(((const uint8_t *)&L.row[of % kListed * KB + row % KB])[row < KB ? 6 : 7]);
+      }
+      *(__attribute__((address_space(3))) u32x4 *)(to + row * ROW + 16 * (chunk ^ f)) = wide(w[0], w[1], power);
+      *(__attribute__((address_space(3))) u32x4 *)(to + row * ROW + 16 * ((chunk + 1) ^ f)) = wide(w[2], w[3], power);
     }
   }
 
@@ -248,12 +267,15 @@ struct Tiled {
 
   // Those values, at the places [p, end), to the rows that see them: whatever
   // their weights were, the sums are then no finite numbers either.
-  static __device__ __forceinline__ void add_not_finite(const AttnArgs &a, f32x16 *o, const Request &rq, int node,
-                                                        const char *v, const int32_t *table, int p, int end, int h) {
-    for (; p < end; p++) {
+  static __device__ __forceinline__ void add_not_finite(const AttnArgs &a, f32x16 *o, const Tile &tile, int node,
+                                                        int near, const char *v, const int32_t *table, int y, int end,
+                                                        int h) {
+    for (; y < end; y++) {
+      const int p = real_place<WIN, KB>(tile, y);
       const uint32_t b = block_of(a, p);
       const int64_t at = row_of(a, p, b, table[b]);
-      if (at < 0 || !(seen(a, rq, node, p, 1) & 1)) continue;
+      if (at < 0 || !(seen(a, tile.q, node, p, 1) & 1)) continue;
+      if (WIN && !(in_window(a, near, p) & 1)) continue;
       const char *row = v + at;
 #pragma unroll
       for (int t = 0; t < DT; t++)
@@ -346,13 +368,14 @@ struct Tiled {
   // The scores of places that a row does not see, to minus infinity; from: the
   // first place that some rows do not see.
   template <int KT>
-  static __device__ __forceinline__ void hide(const AttnArgs &a, f32x16 *s, const Request &rq, int node, int k0,
-                                              int from, const uint32_t *present, uint32_t lane) {
+  static __device__ __forceinline__ void hide(const AttnArgs &a, f32x16 *s, const Request &rq, int node, int near,
+                                              int k0, int from, const uint32_t *present, uint32_t lane) {
     const int h = lane >> 5;
 #pragma unroll
     for (int u = 0; u < KT; u++) {
       uint32_t vis = present[u];
       if (k0 + 32 * KT > from) vis = seen(a, rq, node, k0 + 32 * u, vis);
+      if (WIN) vis &= in_window(a, near, k0 + 32 * u);
       vis >>= 4 * h;
 #pragma unroll
       for (int i = 0; i < 16; i++)
@@ -472,24 +495,26 @@ struct Tiled {
     const int tile_from = a.mask ? ctx : ctx + node_of(a, tile.row0) + 1;
     const int from = a.mask || !any ? ctx : ctx + node_of(a, first_row) + 1;
     const int until = !any ? 0 : a.mask ? rq.len : ctx + node_of(a, min(first_row + 31, rows - 1)) + 1;
-    const int end = min(hi * KB, rq.len);
+    const int end = min(hi * KB, rq.len - (WIN ? tile.skipped * KB : 0));
+    auto real = [&](int j) { return real_place<WIN, KB>(tile, j * KB); };  // where block j begins
     const int half = PAIRED ? 32 * KT * (wave & 1) : 0, late_wave = kPhases && wave >= NW / 2;
     lds_char *buf = (lds_char *)L.buf, *ring = buf + kBuffers * kBuffer;
     int cur = 0, raw = 0;  // the turn's buffer, the ring's place that is fetched into
     if (threadIdx.x == 0) L.odd = 0;
-    uint64_t holes = list(a, L, table, lo & -(kListed / 2), end, 0);  // blocks with places that are not there
+    if (WIN && h == 0) L.near[in_tile] = window_of(a, rq, node);  // (list() has the barrier)
+    uint64_t holes = list(a, L, tile, table, lo & -(kListed / 2), end, 0);  // blocks with places that are not there
 #pragma unroll
     for (int s = 0; s < NS; s++) w.q[s] ^= round;  // (only here are they waited for)
     // Begins turn j: fetches `rows` for a later one, and says where this one's
     // keys and values are, and the next one's.
-    auto begin = [&](const Rows &rows, const lds_char *&now, lds_char *&next) {
+    auto begin = [&](int j, const Rows &rows, const lds_char *&now, lds_char *&next) {
       now = buf + cur * kBuffer + half * ROW;
       if constexpr (F8) {
         fetch(rows, k, v, ring + raw * kRaw, lane, wave);
         raw = raw + 1 == kRaws ? 0 : raw + 1;
         cur = 1 - cur;
         next = buf + cur * kBuffer;
-        widen(ring + raw * kRaw, next);  // the oldest in the ring
+        widen(L, ring + raw * kRaw, next, j + 1, lo);  // the oldest in the ring
       } else {
         fetch(rows, k, v, buf + (cur == 0 ? kBuffers - 1 : cur - 1) * kBuffer, lane, wave);
         cur = cur + 1 == kBuffers ? 0 : cur + 1;
@@ -497,17 +522,23 @@ struct Tiled {
       }
     };
     auto hole = [&](int j) { return (holes >> (j % kListed)) & 1; };
-    auto whole = [&](int j) { return j * KB + KB <= tile_from && !hole(j); };
+    auto whole = [&](int j) {
+      const int p = real(j);
+      return p + KB <= tile_from && !hole(j) && (!WIN || p >= tile.near || p + KB <= a.sinks);
+    };
+    // (WIN: those of the sinks, or those behind them)
+    const int whole_blocks = max(tile_from, 0) / KB, whole_sinks = WIN ? min(a.sinks / KB, whole_blocks) : 0;
     // The turns from j on whose block, and the one before, all rows see whole.
     auto hot = [&](int j, auto late) {
       const int next_list = (j + kAhead + kListed / 2 - 1) & -(kListed / 2);
-      const int stop = min(min(hi, max(tile_from, 0) / KB), next_list - kAhead);
+      const int edge = !WIN ? whole_blocks : j - 1 < whole_sinks ? whole_sinks : whole_blocks - tile.skipped;
+      const int stop = min(min(hi, edge), next_list - kAhead);
       Rows rows = rows_of(L, j + kAhead, lo, lane, wave);
       for (; j < stop && !hole(j); j++) {
         const lds_char *now;
         lds_char *next;
         change_over<kInFlight>();
-        begin(rows, now, next);
+        begin(j, rows, now, next);
         rows = rows_after(L, rows, j + 1 + kAhead, lane, wave);
         if constexpr (!kPhases) {
           if (any) both<KT>(w, now, scale, lane);
@@ -536,22 +567,22 @@ struct Tiled {
         const lds_char *now;
         lds_char *next;
         change_over<kInFlight>();
-        if ((j + kAhead) % (kListed / 2) == 0 && j + kAhead > lo) holes = list(a, L, table, j + kAhead, end, holes);
-        begin(rows_of(L, j + kAhead, lo, lane, wave), now, next);
+        if ((j + kAhead) % (kListed / 2) == 0 && j + kAhead > lo) holes = list(a, L, tile, table, j + kAhead, end, holes);
+        begin(j, rows_of(L, j + kAhead, lo, lane, wave), now, next);
         if (j < lo) continue;
         if (j < hi && !whole(j)) {
           change_over<F8 ? 63 : NL>();
           make_finite(next + kBlock, L.present + j % kListed * (KB / 32), &L.odd);
           change_over<63>();
         }
-        auto use = [&](int j) { return j >= lo && j < hi && j * KB + half < until; };
+        auto use = [&](int j) { return j >= lo && j < hi && real(j) + half < until; };
         for (int phase = 0; phase < 2; phase++) {
           if (phase && kPhases) change_over<63>();
           const int of = late && !phase ? j - 1 : j;  // whose arithmetic
           if (phase == late) products<KT>(w, now, use(j - 1), use(j), l);
           else if (use(of)) {
             if (!whole(of))
-              hide<KT>(a, w.s, rq, node, of * KB + half, from, L.present + (of % kListed * KB + half) / 32, l);
+              hide<KT>(a, w.s, rq, node, WIN ? L.near[in_tile] : 0, real(of) + half, from, L.present + (of % kListed * KB + half) / 32, l);
             weights<KT>(w, scale);
           }
         }
@@ -587,7 +618,7 @@ struct Tiled {
       if (wave & 1) return;
     }
     if (!on) return;
-    if (odd) add_not_finite(a, w.o, rq, node, v, table, lo * KB, end, h);
+    if (odd) add_not_finite(a, w.o, tile, node, WIN ? window_of(a, rq, node) : 0, v, table, lo * KB, end, h);
     if (slot < 0) {
       const float f = sum == 0.f ? 0.f : (a.c.v_scale ? a.c.v_scale[tile.h] : 1.f) / sum;
       const size_t tok = rq.t0 + node;
@@ -616,11 +647,11 @@ struct Tiled {
   }
 };
 
-template <bool BF, bool F8, int D>
+template <bool BF, bool F8, int D, int MODE>
 __global__ __launch_bounds__(kAttnThreads<D>, kAttnWaves<D> / 4) void attn_tile_kernel(AttnArgs a) {
-  using S = Tiled<BF, F8, D>;
+  using S = Tiled<BF, F8, D, MODE>;
   __shared__ typename S::Lds L;
-  walk<S::RT, S::KB, kPairedRows<D>, D, kAttnThreads<D>>(a, [&](const Tile &tile, int lo, int hi, int slot) {
+  walk<S::RT, S::KB, kPairedRows<D>, S::WIN, D, kAttnThreads<D>>(a, [&](const Tile &tile, int lo, int hi, int slot) {
     if constexpr (kPairedRows<D> > 0) {
       if (tile.rows <= kPairedRows<D>) return S::template segment<true>(a, L, tile, lo, hi, slot, gridDim.x);
     }

@@ -33,6 +33,16 @@ struct KvCommitArgs {
 };
 hipError_t launch_kv_commit(const KvCommitArgs &a, hipStream_t s);
 
+struct KvAppendArgs {
+  const uint16_t *k, *v;
+  int64_t k_stride, v_stride;
+  k3_kv_cache c;
+  uint8_t *k_exp, *v_exp;
+  const int32_t *table, *cu, *kv_lens;
+  int dtype, T, blocks, R;
+};
+hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s);
+
 // Attention: q and out are 16-bit rows of the type the kernel is built for.
 struct AttnArgs {
   const uint16_t *q;
@@ -46,12 +56,17 @@ struct AttnArgs {
   // x / d for x < 2^31 is umulhi(2x, magic) >> shift: places by page_size, rows by G
   uint32_t page_magic, group_magic;
   int page_shift, group_shift;
+  int window, sinks;  // a row at position x sees places below sinks, and above x - window (window >= 1)
+  const uint8_t *k_exp, *v_exp;  // of pages and heads, or null
   int slope;        // 16 tile_rows / G
   double inv_groups;  // 1 / workgroups of the launch
 };
 int attn_tile_rows(int T, int G, int R, int D);
 int attn_workgroups(int tile_rows, int D);
 size_t attn_workspace_bytes(int T, int Hq, int n_heads, int D);
-hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t s);
+// The variants of the attention kernels: every place that causality or a mask
+// allows; those in a window; the same over a cache with exponents.
+constexpr int kAllPlaces = 0, kWindow = 1, kBlocks = 2;
+hipError_t launch_attention(const AttnArgs &a, int mode, hipStream_t s);
 
 }  // namespace k3

@@ -13,6 +13,12 @@ hipError_t launch_attn_bf16(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_bf16_e4m3(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_f16(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_f16_e4m3(const AttnArgs &a, hipStream_t s);
+hipError_t launch_attn_bf16_window(const AttnArgs &a, hipStream_t s);
+hipError_t launch_attn_bf16_e4m3_window(const AttnArgs &a, hipStream_t s);
+hipError_t launch_attn_f16_window(const AttnArgs &a, hipStream_t s);
+hipError_t launch_attn_f16_e4m3_window(const AttnArgs &a, hipStream_t s);
+hipError_t launch_attn_bf16_blocks(const AttnArgs &a, hipStream_t s);
+hipError_t launch_attn_f16_blocks(const AttnArgs &a, hipStream_t s);
 
 // Rows per tile: up to 32 rows of an average request (16 at a head of 256) go
 // to the streaming kernel, more to the tiled kernel. Streaming (its better
@@ -64,9 +70,14 @@ size_t attn_workspace_bytes(int T, int Hq, int n_heads, int D) {
   return rows * (D + 2) * sizeof(float) + kMaxWorkgroups * sizeof(JoinJob);
 }
 
-hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t s) {
-  const bool f8 = a.c.dtype == K3_E4M3;
-  if (a.dtype == K3_BF16) return f8 ? launch_attn_bf16_e4m3(a, s) : launch_attn_bf16(a, s);
+hipError_t launch_attention(const AttnArgs &a, int mode, hipStream_t s) {
+  const bool f8 = a.c.dtype == K3_E4M3, bf = a.dtype == K3_BF16;
+  if (mode == kBlocks) return bf ? launch_attn_bf16_blocks(a, s) : launch_attn_f16_blocks(a, s);
+  if (mode == kWindow) {
+    if (bf) return f8 ? launch_attn_bf16_e4m3_window(a, s) : launch_attn_bf16_window(a, s);
+    return f8 ? launch_attn_f16_e4m3_window(a, s) : launch_attn_f16_window(a, s);
+  }
+  if (bf) return f8 ? launch_attn_bf16_e4m3(a, s) : launch_attn_bf16(a, s);
   return f8 ? launch_attn_f16_e4m3(a, s) : launch_attn_f16(a, s);
 }
 
@@ -246,11 +257,13 @@ size_t k3_tree_attention_workspace_bytes(int T, int Hq, int n_heads, int head_di
   return attn_workspace_bytes(std::max(T, 1), Hq, n_heads, head_dim);
 }
 
-k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T, int Hq, const k3_kv_cache *cache,
-                            const int32_t *table, int blocks, const int32_t *cu, const int32_t *kv_lens, int R,
-                            const int32_t *mask, int words, float scale, void *out, int64_t out_stride, void *ws,
-                            size_t ws_bytes, float *lse, k3_stream_t stream) {
-  const char *fn = "k3_tree_attention";
+// The attention calls. window: 0 for none; k_exp, v_exp: of a cache with
+// exponents, or null.
+static k3_status attention(const char *fn, const void *q, int64_t q_stride, int dtype, int T, int Hq,
+                           const k3_kv_cache *cache, const uint8_t *k_exp, const uint8_t *v_exp, const int32_t *table,
+                           int blocks, const int32_t *cu, const int32_t *kv_lens, int R, const int32_t *mask, int words,
+                           int window, int sinks, float scale, void *out, int64_t out_stride, void *ws,
+                           size_t ws_bytes, float *lse, k3_stream_t stream) {
   if (k3_status s = check_cache(fn, cache)) return s;
   KV_NEED(dtype == K3_BF16 || dtype == K3_F16, "%s: dtype=%d is neither K3_BF16 nor K3_F16", fn, dtype);
   KV_NEED(cache->dtype == K3_E4M3 || cache->dtype == dtype, "%s: a cache of dtype=%d for rows of dtype=%d", fn,
@@ -259,6 +272,10 @@ k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T, i
   if (k3_status s = check_table(fn, R, blocks, cache->page_size)) return s;
   KV_NEED(!mask || (words >= 1 && words <= K3_MAX_TREE_WORDS), "%s: words=%d outside [1, %d]", fn, words,
           K3_MAX_TREE_WORDS);
+  KV_NEED(window >= 0 && window <= 1 << 30 && sinks >= 0 && sinks <= 1 << 30,
+          "%s: window=%d, sinks=%d: neither negative nor above 2^30", fn, window, sinks);
+  KV_NEED(!mask || !window || window >= 32 * words, "%s: window=%d is below the %d nodes that a mask of %d words has", fn,
+          window, 32 * words, words);
   KV_NEED(isfinite(scale), "%s: scale=%g must be finite", fn, scale);
   KV_PTR(table, 4);
   KV_PTR(cu, 4);
@@ -297,6 +314,10 @@ k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T, i
   a.blocks = blocks;
   a.R = R;
   a.words = words;
+  a.window = window ? window : 1 << 30;
+  a.sinks = window ? sinks : 0;
+  a.k_exp = k_exp;
+  a.v_exp = v_exp;
   // x / d = (x * m) >> (31 + s) for x < 2^31: s = ceil(log2 d), m the next
   // integer above 2^(31 + s) / d (m < 2^32, and m d - 2^(31 + s) <= 2^s)
   auto divisor = [](int d, uint32_t *magic, int *shift) {
@@ -311,7 +332,80 @@ k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T, i
   a.part_rows = attn_part_rows(tile_rows, T, a.G);
   a.slope = 16 * tile_rows / a.G;
   a.inv_groups = 1.0 / attn_workgroups(tile_rows, D);
-  return device_status(launch_tree_attention(a, stream), fn);
+  return device_status(launch_attention(a, k_exp ? kBlocks : window ? kWindow : kAllPlaces, stream), fn);
+}
+
+k3_status k3_tree_attention(const void *q, int64_t q_stride, int dtype, int T, int Hq, const k3_kv_cache *cache,
+                            const int32_t *table, int blocks, const int32_t *cu, const int32_t *kv_lens, int R,
+                            const int32_t *mask, int words, float scale, void *out, int64_t out_stride, void *ws,
+                            size_t ws_bytes, float *lse, k3_stream_t stream) {
+  return attention("k3_tree_attention", q, q_stride, dtype, T, Hq, cache, nullptr, nullptr, table, blocks, cu, kv_lens,
+                   R, mask, words, 0, 0, scale, out, out_stride, ws, ws_bytes, lse, stream);
+}
+
+k3_status k3_window_attention(const void *q, int64_t q_stride, int dtype, int T, int Hq, const k3_kv_cache *cache,
+                              const int32_t *table, int blocks, const int32_t *cu, const int32_t *kv_lens, int R,
+                              const int32_t *mask, int words, int window, int sinks, float scale, void *out,
+                              int64_t out_stride, void *ws, size_t ws_bytes, float *lse, k3_stream_t stream) {
+  return attention("k3_window_attention", q, q_stride, dtype, T, Hq, cache, nullptr, nullptr, table, blocks, cu,
+                   kv_lens, R, mask, words, window, sinks, scale, out, out_stride, ws, ws_bytes, lse, stream);
+}
+
+// A cache whose scales are exponents of pages and heads.
+static k3_status check_exponents(const char *fn, const k3_kv_cache *cache, const uint8_t *k_exp, const uint8_t *v_exp) {
+  if (k3_status s = check_cache(fn, cache)) return s;
+  KV_PTR(k_exp, 1);
+  KV_PTR(v_exp, 1);
+  KV_NEED(k_exp != v_exp, "%s: k_exp is v_exp", fn);
+  KV_NEED(cache->dtype == K3_E4M3 && !cache->k_scale && !cache->v_scale,
+          "%s: exponents go with an e4m3 cache without scales (cache dtype=%d)", fn, cache->dtype);
+  KV_NEED(cache->page_size % 4 == 0, "%s: page_size=%d must be a multiple of 4", fn, cache->page_size);
+  return K3_OK;
+}
+
+k3_status k3_block_attention(const void *q, int64_t q_stride, int dtype, int T, int Hq, const k3_kv_cache *cache,
+                             const uint8_t *k_exp, const uint8_t *v_exp, const int32_t *table, int blocks,
+                             const int32_t *cu, const int32_t *kv_lens, int R, int window, int sinks, float scale,
+                             void *out, int64_t out_stride, void *ws, size_t ws_bytes, float *lse,
+                             k3_stream_t stream) {
+  const char *fn = "k3_block_attention";
+  if (k3_status s = check_exponents(fn, cache, k_exp, v_exp)) return s;
+  return attention(fn, q, q_stride, dtype, T, Hq, cache, k_exp, v_exp, table, blocks, cu, kv_lens, R, nullptr, 0,
+                   window, sinks, scale, out, out_stride, ws, ws_bytes, lse, stream);
+}
+
+k3_status k3_kv_append(const void *k_in, int64_t k_stride, const void *v_in, int64_t v_stride, int dtype, int T,
+                       const k3_kv_cache *cache, uint8_t *k_exp, uint8_t *v_exp, const int32_t *table, int blocks,
+                       const int32_t *cu, const int32_t *kv_lens, int R, k3_stream_t stream) {
+  const char *fn = "k3_kv_append";
+  if (k3_status s = check_exponents(fn, cache, k_exp, v_exp)) return s;
+  KV_NEED(dtype == K3_BF16 || dtype == K3_F16, "%s: dtype=%d is neither K3_BF16 nor K3_F16", fn, dtype);
+  KV_NEED(T >= 0 && T <= kMaxTokens, "%s: T=%d outside [0, %d]", fn, T, kMaxTokens);
+  if (k3_status s = check_table(fn, R, blocks, cache->page_size)) return s;
+  KV_PTR(table, 4);
+  KV_PTR(cu, 4);
+  KV_PTR(kv_lens, 4);
+  if (T == 0) return K3_OK;
+  KV_PTR(k_in, 16);
+  KV_PTR(v_in, 16);
+  if (k3_status s = check_rows(fn, "k_stride", k_stride, T, cache->n_heads, cache->head_dim)) return s;
+  if (k3_status s = check_rows(fn, "v_stride", v_stride, T, cache->n_heads, cache->head_dim)) return s;
+  KvAppendArgs a = {};
+  a.k = (const uint16_t *)k_in;
+  a.v = (const uint16_t *)v_in;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.c = *cache;
+  a.k_exp = k_exp;
+  a.v_exp = v_exp;
+  a.table = table;
+  a.cu = cu;
+  a.kv_lens = kv_lens;
+  a.dtype = dtype;
+  a.T = T;
+  a.blocks = blocks;
+  a.R = R;
+  return device_status(launch_kv_append(a, stream), fn);
 }
 
 static k3_status commit(const char *fn, const k3_kv_cache *cache, int layers, int64_t layer_stride,

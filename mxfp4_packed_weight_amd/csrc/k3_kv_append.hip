@@ -1,0 +1,171 @@
+// The append to an e4m3 cache with an exponent for each page and head.
+//
+//   e = ceil(log2(max |x| / 448)) over the page's new rows, not below that of
+//   rows that the page has already;  code = e4m3(x 2^-e)
+// A wave takes a page's new rows of one head, keys and values: it reads them
+// once, keeps them in registers while it finds the largest (pages of more than
+// kKeep loads are read again, out of the caches), and writes the codes. Only if
+// the exponent rises are the page's earlier codes read and rounded again. Which
+// page of which request follows without a prefix sum: n tokens touch at most
+// n / P + 2 pages, so that request r's are among the numbers from cu[r] / P + 2 r
+// on, and a search by 64 finds r.
+#include "k3_kv.h"
+#include "k3_rows.h"
+
+namespace k3 {
+
+namespace {
+
+constexpr int kAppendWaves = 4;
+constexpr int kKeep = 8;  // loads of a lane, keys and values alike
+
+// Eight values' largest size; infinities and NaN do not count.
+template <bool BF>
+__device__ __forceinline__ float largest(const uint4 &x, float top) {
+  float f[8];
+  unpack8<BF>(x, f);
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    const float y = fabsf(f[j]);
+    top = y < INFINITY ? fmaxf(top, y) : top;
+  }
+  return top;
+}
+// The byte e + 127 of the smallest 2^e with amax <= 448 2^e = 1.75 2^(e + 8).
+__device__ __forceinline__ int exponent_of(float amax) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, amax);
+  return max((int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u), 1);
+}
+template <bool BF>
+__device__ __forceinline__ uint2 codes_of(const uint4 &x, int byte) {
+  float f[8];
+  unpack8<BF>(x, f);
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    // (fp16: 448 2^7 < 61440 = 240 2^8 < 65504, which would round to 2^16)
+    float y = f[j];
+    if (!BF) y = y != y ? y : fminf(fmaxf(y, -61440.f), 61440.f);
+    y = ldexpf(y, 127 - byte);
+    f[j] = y != y ? y : fminf(fmaxf(y, -448.f), 448.f);
+  }
+  return to_e4m3(f);
+}
+// Codes times 2^-fall, rounded again.
+__device__ __forceinline__ uint2 lowered(uint2 w, int fall) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const int x = i ? w.y : w.x;
+    f[4 * i] = __builtin_amdgcn_cvt_f32_fp8(x, 0);
+    f[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8(x, 1);
+    f[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8(x, 2);
+    f[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8(x, 3);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; j++) f[j] = ldexpf(f[j], -fall);
+  return to_e4m3(f);
+}
+
+template <bool BF, int D>
+__global__ __launch_bounds__(64 * kAppendWaves) void kv_append_kernel(KvAppendArgs a, int items) {
+  constexpr int LPR = D / 8, RPL = 64 / LPR;  // lanes of a row, rows of a load
+  const int lane = threadIdx.x & 63, sub = lane / LPR, d0 = lane % LPR * 8;
+  const int H = a.c.n_heads, P = a.c.page_size;
+  // (below 2^29: T / 4 and 2 R items, 2^10 heads)
+  const int unit = __builtin_amdgcn_readfirstlane(blockIdx.x * kAppendWaves + (threadIdx.x >> 6));
+  const int item = unit / H, h = unit - item * H;
+  if (item >= items) return;
+  auto start = [&](int r) { return min(max(a.cu[r], 0), a.T) / P + 2 * r; };
+  // the last request that starts at or before the item
+  int r = 0;
+  for (int n = a.R; n > 1;) {
+    const int step = (n + 63) / 64;
+    const uint64_t at = __ballot(lane * step < n && start(min(r + lane * step, a.R - 1)) <= item);
+    if (!at) return;
+    const int last = 63 - __builtin_clzll(at);
+    r += last * step;
+    n = min(step, n - last * step);
+  }
+  const int t0 = a.cu[r], len = a.kv_lens[r];
+  const int64_t n = (int64_t)a.cu[r + 1] - t0;
+  if (t0 < 0 || n <= 0 || t0 + n > a.T || len < n || len > a.blocks * P) return;
+  const int ctx = len - (int)n, j = item - (t0 / P + 2 * r), b = ctx / P + j;
+  if (j < 0 || b > (len - 1) / P) return;
+  const int page = a.table[(int64_t)r * a.blocks + b];
+  if (page < 0 || page >= a.c.n_pages) return;
+  const int first = max(ctx, b * P), rows = min(len, b * P + P) - first, earlier = first - b * P;
+  const int t = t0 + first - ctx;
+  const uint16_t *in[2] = {a.k + t * a.k_stride + h * D + d0, a.v + t * a.v_stride + h * D + d0};
+  const int64_t in_stride[2] = {a.k_stride, a.v_stride};
+  const int64_t at = page * a.c.page_stride + h * a.c.head_stride + d0;
+  uint8_t *out[2] = {(uint8_t *)a.c.k + at, (uint8_t *)a.c.v + at};
+  uint8_t *exps[2] = {a.k_exp + (int64_t)page * H + h, a.v_exp + (int64_t)page * H + h};
+
+  uint4 x[2][kKeep];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < kKeep; i++)
+#pragma unroll
+      for (int s = 0; s < 2; s++) {
+        const int row = i0 + i * RPL + sub;
+        x[s][i] = uint4{0, 0, 0, 0};
+        if (row < rows) x[s][i] = *(const uint4 *)(in[s] + row * in_stride[s]);
+      }
+  };
+  int was[2] = {0, 0};  // the earlier rows' exponents
+  if (earlier)
+#pragma unroll
+    for (int s = 0; s < 2; s++) was[s] = min(max((int)*exps[s], 1), 254);
+  constexpr int CHUNK = kKeep * RPL;
+  float top[2] = {0.f, 0.f};
+  for (int i0 = 0; i0 < rows; i0 += CHUNK) {
+    load(i0);
+#pragma unroll
+    for (int i = 0; i < kKeep; i++)
+#pragma unroll
+      for (int s = 0; s < 2; s++) top[s] = largest<BF>(x[s][i], top[s]);
+  }
+  int byte[2];
+#pragma unroll
+  for (int s = 0; s < 2; s++) {
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) top[s] = fmaxf(top[s], __shfl_xor(top[s], m));
+    byte[s] = max(exponent_of(top[s]), was[s]);
+    if (lane == 0) *exps[s] = (uint8_t)byte[s];
+    if (earlier && byte[s] > was[s])
+      for (int row = sub; row < earlier; row += RPL) {
+        uint2 *p = (uint2 *)(out[s] + row * a.c.slot_stride);
+        *p = lowered(*p, byte[s] - was[s]);
+      }
+  }
+  for (int i0 = 0; i0 < rows; i0 += CHUNK) {
+    if (rows > CHUNK) load(i0);
+#pragma unroll
+    for (int i = 0; i < kKeep; i++)
+#pragma unroll
+      for (int s = 0; s < 2; s++) {
+        const int row = i0 + i * RPL + sub;
+        if (row < rows) *(uint2 *)(out[s] + (earlier + row) * a.c.slot_stride) = codes_of<BF>(x[s][i], byte[s]);
+      }
+  }
+}
+
+template <bool BF>
+hipError_t by_dim(const KvAppendArgs &a, hipStream_t s) {
+  const int items = a.T / a.c.page_size + 2 * a.R;
+  const unsigned grid = (unsigned)(((int64_t)items * a.c.n_heads + kAppendWaves - 1) / kAppendWaves);
+  switch (a.c.head_dim) {
+    case 64: kv_append_kernel<BF, 64><<<grid, 64 * kAppendWaves, 0, s>>>(a, items); break;
+    case 128: kv_append_kernel<BF, 128><<<grid, 64 * kAppendWaves, 0, s>>>(a, items); break;
+    default: kv_append_kernel<BF, 256><<<grid, 64 * kAppendWaves, 0, s>>>(a, items);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s) {
+  return a.dtype == K3_BF16 ? by_dim<true>(a, s) : by_dim<false>(a, s);
+}
+
+}  // namespace k3
