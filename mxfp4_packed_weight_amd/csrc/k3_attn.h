@@ -17,7 +17,9 @@
 //
 // Windows. A row at position x sees the places below `sinks` and those above
 // x - window. Of a tile's places only the blocks up to the sinks' end and from
-// its first row's window on are taken: they are numbered without the gap, and
+// its first row's window on are taken: they are numbered without the gap, as
+// if the request were so much shorter (its rows' positions and windows with
+// it; what is below the gap is seen by the sinks' rule alone), and
 // real_place() turns such a place into the cache's.
 #pragma once
 
@@ -181,13 +183,18 @@ struct Tile {
   long long first, after;  // its stretch of the line
   int tiles;               // of its key head
   // WIN: blocks of the sinks, blocks that are left out behind them, the first
-  // place that is in the window of all rows
+  // place (without the gap) that is in the window of all rows
   int sink_blocks, skipped, near;
 };
-// Place y of a tile's, counted without the gap, in the cache.
+// Place y of a tile's, counted without the gap, in the cache; and the request
+// as it is without the gap.
 template <bool WIN, int KB>
 __device__ __forceinline__ int real_place(const Tile &t, int y) {
   return WIN && y >= t.sink_blocks * KB ? y + t.skipped * KB : y;
+}
+template <bool WIN, int KB>
+__device__ __forceinline__ Request without_gap(const Tile &t) {
+  return {t.q.t0, t.q.n, t.q.len - (WIN ? t.skipped * KB : 0)};
 }
 // The rest of a tile from q, r, h, x and first.
 template <int RT, int KB, int HALF, bool WIN>
@@ -203,10 +210,11 @@ __device__ __forceinline__ void fill_tile(const AttnArgs &a, Tile &t, const Cost
   if constexpr (WIN) {
     // (a tree's row is at its request's last committed place or later)
     const int ctx = t.q.len - t.q.n, first = a.mask ? ctx - 1 : ctx + node_of(a, t.row0);
-    t.near = t.places - a.window;
     t.sink_blocks = (min(a.sinks, max(t.places, 0)) + KB - 1) / KB;
     t.skipped = max(0, min(max(0, first - a.window + 1) / KB, t.blocks - 1) - t.sink_blocks);
     t.blocks -= t.skipped;
+    t.places -= t.skipped * KB;
+    t.near = t.places - a.window;
   }
 }
 // The tile that place u of the line is in.
@@ -261,6 +269,16 @@ __device__ __forceinline__ void next_tile(const AttnArgs &a, const Line<THREADS>
     }
   }
   fill_tile<RT, KB, HALF, WIN>(a, t, Cost<RT, HALF, WIN>(a, t.q));
+}
+
+// The same in scalar registers: what was worked out in fp64 is in vector ones
+// otherwise, of which the walk holds more than it has with a window.
+__device__ __forceinline__ void to_scalars(Tile &t) {
+  for (int *x : {&t.q.t0, &t.q.n, &t.q.len, &t.r, &t.h, &t.x, &t.row0, &t.rows, &t.places, &t.blocks, &t.weight,
+                 &t.tiles, &t.sink_blocks, &t.skipped, &t.near})
+    *x = __builtin_amdgcn_readfirstlane(*x);
+  t.first = in_all_lanes(t.first);
+  t.after = in_all_lanes(t.after);
 }
 
 // The tile's first block that is done after place u of the line (any rising
@@ -326,6 +344,7 @@ __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
   for (long long u = begin; u < end;) {
     if (u == begin) tile = tile_at<RT, KB, HALF, WIN>(a, L, u);
     else next_tile<RT, KB, HALF, WIN>(a, L, tile);
+    if constexpr (WIN) to_scalars(tile);
     const int lo = block_from<RT, KB>(tile, u), hi = block_from<RT, KB>(tile, end);
     const int slot = lo == hi || (lo == 0 && hi == tile.blocks) ? -1 : lo ? 2 * b : 2 * b + 1;
     if (u > tile.first) job.head_slot = slot;

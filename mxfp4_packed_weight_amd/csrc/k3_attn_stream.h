@@ -250,11 +250,10 @@ struct Stream {
 
   // One run of 32 places: scores, weights, and the weighted values.
   template <int RUN>
-  static __device__ __forceinline__ void run(const AttnArgs &a, Wave &w, const Tile &tile, const int *node,
-                                             const int *near, int k0, float scale, const char *v,
+  static __device__ __forceinline__ void run(const AttnArgs &a, Wave &w, const Request &rq, int all_near,
+                                             const int *node, const int *near, int k0, float scale, const char *v,
                                              const int64_t *offset, const float (*power)[BLK ? PLACES : 1],
                                              float *scratch, int c, int g) {
-    const Request &rq = tile.q;
     float k_power[2] = {1.f, 1.f}, v_power[2] = {1.f, 1.f};
     if constexpr (BLK) {
 #pragma unroll
@@ -278,7 +277,7 @@ struct Stream {
       }
     const uint32_t present = w.present[RUN];
     // places that some rows may not see
-    const bool drafts = k0 + 32 > rq.len - rq.n || (WIN && k0 < tile.near && k0 + 32 > a.sinks);
+    const bool drafts = k0 + 32 > rq.len - rq.n || (WIN && k0 < all_near && k0 + 32 > a.sinks);
     const bool partial = drafts || present != 0xffffffffu;
     bool odd = false;
     if (partial) {
@@ -352,7 +351,7 @@ struct Stream {
   static __device__ __forceinline__ void segment(const AttnArgs &a, Lds &L, const Tile &tile, int lo, int hi,
                                                  int slot, int B) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
-    const Request &rq = tile.q;
+    const Request shorter = without_gap<WIN, KB>(tile), &rq = WIN ? shorter : tile.q;
     const int rows = rq.n * a.G;
     Wave w;
     int node[QT], near[QT];
@@ -376,14 +375,14 @@ struct Stream {
     const char *v = (const char *)a.c.v + tile.h * a.c.head_stride * ES;
     const int32_t *table = a.table + (size_t)tile.r * a.blocks;
     int64_t *offset = L.offset[wave];
-    const int end = (int)min((long long)hi * KB, (long long)tile.places - (WIN ? tile.skipped * KB : 0));
+    const int end = (int)min((long long)hi * KB, (long long)tile.places);
     auto real = [&](int y) { return real_place<WIN, KB>(tile, y); };  // (a wave's places are in one block)
     int k0 = lo * KB + PLACES * wave;
-    int page = table_entry(a, table, real(k0) + lane % PLACES, rq.len);
+    int page = table_entry(a, table, real(k0) + lane % PLACES, tile.q.len);
     if (k0 < end) {
       places(a, w, offset, lane, tile.h, real(k0), page);
       load(w, k, v, offset, c, g);
-      page = table_entry(a, table, real(k0 + KB) + lane % PLACES, rq.len);
+      page = table_entry(a, table, real(k0 + KB) + lane % PLACES, tile.q.len);
       for (; k0 < end; k0 += KB) {
         if constexpr (BLK) {
           if (lane < PLACES) {
@@ -392,13 +391,13 @@ struct Stream {
           }
           wave_sync();
         }
-        run<0>(a, w, tile, node, near, real(k0), scale, v, offset, L.power[wave], L.o[wave], c, g);
+        run<0>(a, w, rq, tile.near, node, near, k0, scale, v, offset, L.power[wave], L.o[wave], c, g);
         if (RUNS > 1 && k0 + 32 < end)
-          run<RUNS - 1>(a, w, tile, node, near, real(k0) + 32, scale, v, offset + PLACES - 32, L.power[wave],
+          run<RUNS - 1>(a, w, rq, tile.near, node, near, k0 + 32, scale, v, offset + PLACES - 32, L.power[wave],
                         L.o[wave], c, g);
         if (k0 + KB < end) {
           places(a, w, offset, lane, tile.h, real(k0 + KB), page);
-          page = table_entry(a, table, real(k0 + 2 * KB) + lane % PLACES, rq.len);
+          page = table_entry(a, table, real(k0 + 2 * KB) + lane % PLACES, tile.q.len);
           load(w, k, v, offset, c, g);
         }
       }

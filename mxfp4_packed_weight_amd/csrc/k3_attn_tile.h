@@ -268,14 +268,15 @@ struct Tiled {
   // Those values, at the places [p, end), to the rows that see them: whatever
   // their weights were, the sums are then no finite numbers either.
   static __device__ __forceinline__ void add_not_finite(const AttnArgs &a, f32x16 *o, const Tile &tile, int node,
-                                                        int near, const char *v, const int32_t *table, int y, int end,
-                                                        int h) {
+                                                        const char *v, const int32_t *table, int y, int end, int h) {
+    const Request rq = without_gap<WIN, KB>(tile);
+    const int near = WIN ? window_of(a, rq, node) : 0;
     for (; y < end; y++) {
       const int p = real_place<WIN, KB>(tile, y);
       const uint32_t b = block_of(a, p);
       const int64_t at = row_of(a, p, b, table[b]);
-      if (at < 0 || !(seen(a, tile.q, node, p, 1) & 1)) continue;
-      if (WIN && !(in_window(a, near, p) & 1)) continue;
+      if (at < 0 || !(seen(a, rq, node, y, 1) & 1)) continue;
+      if (WIN && !(in_window(a, near, y) & 1)) continue;
       const char *row = v + at;
 #pragma unroll
       for (int t = 0; t < DT; t++)
@@ -467,7 +468,7 @@ struct Tiled {
                                                  int B) {
     const uint32_t lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Request &rq = tile.q;
+    const Request shorter = without_gap<WIN, KB>(tile), &rq = WIN ? shorter : tile.q;
     const int first_in_tile = 32 * (PAIRED ? wave >> 1 : wave), in_tile = first_in_tile + (int)c;
     const int rows = rq.n * a.G, first_row = tile.row0 + first_in_tile, row = tile.row0 + in_tile;
     const bool on = row < rows, any = first_row < rows;
@@ -495,8 +496,7 @@ struct Tiled {
     const int tile_from = a.mask ? ctx : ctx + node_of(a, tile.row0) + 1;
     const int from = a.mask || !any ? ctx : ctx + node_of(a, first_row) + 1;
     const int until = !any ? 0 : a.mask ? rq.len : ctx + node_of(a, min(first_row + 31, rows - 1)) + 1;
-    const int end = min(hi * KB, rq.len - (WIN ? tile.skipped * KB : 0));
-    auto real = [&](int j) { return real_place<WIN, KB>(tile, j * KB); };  // where block j begins
+    const int end = min(hi * KB, rq.len);
     const int half = PAIRED ? 32 * KT * (wave & 1) : 0, late_wave = kPhases && wave >= NW / 2;
     lds_char *buf = (lds_char *)L.buf, *ring = buf + kBuffers * kBuffer;
     int cur = 0, raw = 0;  // the turn's buffer, the ring's place that is fetched into
@@ -523,15 +523,14 @@ struct Tiled {
     };
     auto hole = [&](int j) { return (holes >> (j % kListed)) & 1; };
     auto whole = [&](int j) {
-      const int p = real(j);
-      return p + KB <= tile_from && !hole(j) && (!WIN || p >= tile.near || p + KB <= a.sinks);
+      return j * KB + KB <= tile_from && !hole(j) && (!WIN || j * KB >= tile.near || j * KB + KB <= a.sinks);
     };
     // (WIN: those of the sinks, or those behind them)
     const int whole_blocks = max(tile_from, 0) / KB, whole_sinks = WIN ? min(a.sinks / KB, whole_blocks) : 0;
     // The turns from j on whose block, and the one before, all rows see whole.
     auto hot = [&](int j, auto late) {
       const int next_list = (j + kAhead + kListed / 2 - 1) & -(kListed / 2);
-      const int edge = !WIN ? whole_blocks : j - 1 < whole_sinks ? whole_sinks : whole_blocks - tile.skipped;
+      const int edge = !WIN ? whole_blocks : j - 1 < whole_sinks ? whole_sinks : whole_blocks;
       const int stop = min(min(hi, edge), next_list - kAhead);
       Rows rows = rows_of(L, j + kAhead, lo, lane, wave);
       for (; j < stop && !hole(j); j++) {
@@ -575,14 +574,14 @@ struct Tiled {
           make_finite(next + kBlock, L.present + j % kListed * (KB / 32), &L.odd);
           change_over<63>();
         }
-        auto use = [&](int j) { return j >= lo && j < hi && real(j) + half < until; };
+        auto use = [&](int j) { return j >= lo && j < hi && j * KB + half < until; };
         for (int phase = 0; phase < 2; phase++) {
           if (phase && kPhases) change_over<63>();
           const int of = late && !phase ? j - 1 : j;  // whose arithmetic
           if (phase == late) products<KT>(w, now, use(j - 1), use(j), l);
           else if (use(of)) {
             if (!whole(of))
-              hide<KT>(a, w.s, rq, node, WIN ? L.near[in_tile] : 0, real(of) + half, from, L.present + (of % kListed * KB + half) / 32, l);
+              hide<KT>(a, w.s, rq, node, WIN ? L.near[in_tile] : 0, of * KB + half, from, L.present + (of % kListed * KB + half) / 32, l);
             weights<KT>(w, scale);
           }
         }
@@ -618,7 +617,7 @@ struct Tiled {
       if (wave & 1) return;
     }
     if (!on) return;
-    if (odd) add_not_finite(a, w.o, tile, node, WIN ? window_of(a, rq, node) : 0, v, table, lo * KB, end, h);
+    if (odd) add_not_finite(a, w.o, tile, node, v, table, lo * KB, end, h);
     if (slot < 0) {
       const float f = sum == 0.f ? 0.f : (a.c.v_scale ? a.c.v_scale[tile.h] : 1.f) / sum;
       const size_t tok = rq.t0 + node;
