@@ -26,6 +26,7 @@
 #include <math.h>
 
 #include "k3_kv.h"
+#include "k3_lanes.h"
 
 namespace k3 {
 
@@ -412,12 +413,6 @@ template <bool BF>
 __device__ __forceinline__ float half_at(uint32_t w, int hi) {
   if (BF) return __builtin_bit_cast(float, hi ? w & 0xffff0000u : w << 16);
   return (float)__builtin_bit_cast(f16x2, w)[hi];
-}
-// Orders a wave's own LDS accesses, which its lanes share (LDS serves a
-// wave's accesses in order; this keeps the compiler to that order).
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
 }
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 

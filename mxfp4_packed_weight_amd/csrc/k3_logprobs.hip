@@ -5,20 +5,27 @@
 // for a reference m that is at least near the largest of what was read so far:
 // one pass, S and Q are scaled when m rises. Differences are taken before the
 // factor beta, so that logits of the type's lowest value still differ by 0 from
-// one another. In e^d d an x of
-// -inf counts as the lowest number, times 0.
+// one another. In e^d d an x of -inf counts as the lowest number, times 0.
 //
-// A row's logits go to the waves in runs of 64 lanes x 2 loads of 16 bytes. Each
-// wave keeps the k <= 64 largest of its logits sorted in its lanes, one a lane:
-// only a logit above the k-th is looked at, from the lowest lane on, which
-// leaves equal ones in the order of their indices. The first run's threshold is
-// the k-th largest of the lanes' own maxima. Lists join by comparing one with
-// another turned round, which leaves the largest 64 of both, and six steps of
-// sorting.
+// A row's logits go to the waves in runs of 64 lanes x 16. Each wave keeps the
+// k <= 64 largest of its logits sorted in its lanes, one a lane. The logits of a
+// run that are above the k-th are collected in LDS, and when 64 are there they are
+// sorted and joined with the list: a comparison of one list with the other turned
+// round leaves the largest 64 of both, six steps of sorting order them. (Putting
+// them in one by one took four times as long: 64 rows of 131072 logits with 20
+// alternatives 41 -> 24 us.) Until a wave has k, a run's threshold is the k-th
+// largest of its lanes' own maxima.
+//
+// 1000 rows of 150001 fp32 logits, 600 MB: 91 us, 6.6 TB/s (a plain read reaches
+// 7.1); with 20 alternatives 102 us. Rows of 16 bits are bound by the vector unit
+// (a dozen instructions to a logit, one of them an exponential at a quarter of the
+// rate): 56 us, 5.3 TB/s, 82 with 20 alternatives. One row of 131072: 11 us, two
+// launches' latency. Runs further ahead than the next change nothing.
 #include <math.h>
 
 #include <algorithm>
 
+#include "k3_lanes.h"
 #include "k3_rows.h"
 #include "k3_step.h"
 
@@ -27,14 +34,14 @@ namespace k3 {
 namespace {
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves, kJoinWaves = 8;
-constexpr int kLoads = 2;  // of a lane in a run
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.4028234663852886e38f;
 
 template <int TYPE>
 constexpr int kPer = TYPE == K3_F32 ? 4 : 8;  // values of 16 bytes
 template <int TYPE>
-constexpr int kRun = 64 * kLoads * kPer<TYPE>;
+constexpr int kLoads = 16 / kPer<TYPE>;  // of a lane in a run
+constexpr int kRun = 64 * 16;            // values of a run
 
 template <int TYPE>
 __device__ __forceinline__ float value_at(const void *row, int64_t i) {
@@ -73,59 +80,70 @@ struct Sums {
     s += o.s;
     q += o.q;
   }
+  __device__ __forceinline__ void join_lanes(float b2) {
+    halving<32>([&](auto d) {
+      constexpr int D = decltype(d)::value;
+      join(Sums{lane_xor<D>(m), lane_xor<D>(s), lane_xor<D>(q)}, b2);
+    });
+  }
 };
 
 // ---- lists of the largest -------------------------------------------------------
 
-// Lane j has the j-th largest, or (-inf, INT_MAX).
-struct List {
-  float v;
-  int at;
-};
-// Greater values first, of equal ones the lower index.
-__device__ __forceinline__ bool before(const List &x, const List &y) {
-  return x.v > y.v || (x.v == y.v && x.at < y.at);
-}
-__device__ __forceinline__ float of_lane(float x, int lane) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
-}
-// The largest 64 of both.
-__device__ __forceinline__ List joined(List x, const List &y, int lane) {
-  List o = {__shfl(y.v, 63 - lane), __shfl(y.at, 63 - lane)};
-  if (before(o, x)) x = o;
-#pragma unroll
-  for (int d = 32; d; d /= 2) {
-    o = List{__shfl_xor(x.v, d), __shfl_xor(x.at, d)};
-    if (before(o, x) == !(lane & d)) x = o;
-  }
-  return x;
-}
-// A list of any 64 entries.
-__device__ __forceinline__ List sorted(List x, int lane) {
-#pragma unroll
-  for (int n = 2; n <= 64; n *= 2)
-#pragma unroll
-    for (int d = n / 2; d; d /= 2) {
-      const List o = {__shfl_xor(x.v, d), __shfl_xor(x.at, d)};
-      if (before(o, x) == (!(lane & d) == !(lane & n))) x = o;
-    }
-  return x;
-}
-// Puts a value in (all lanes the same; larger than the list's last).
-__device__ __forceinline__ void insert(List &x, float v, int at, int lane) {
-  const int place = __popcll(__ballot(x.v >= v));
-  const float pv = __shfl_up(x.v, 1);
-  const int pat = __shfl_up(x.at, 1);
-  if (lane > place) x = List{pv, pat};
-  if (lane == place) x = List{v, at};
-}
-// Rising integers for rising floats, and back.
+// A logit and its index as one number, larger for what comes first: greater
+// values, of equal ones the lower index.
+typedef uint64_t Entry;
+// Rising integers for rising floats (no NaN), and back.
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float from_ordered(uint32_t u) {
   return __builtin_bit_cast(float, u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+__device__ __forceinline__ Entry entry_of(float v, int at) {
+  return (uint64_t)ordered(v + 0.f) << 32 | ~(uint32_t)at;  // (no -0)
+}
+constexpr Entry kNone = (uint64_t)0x007fffffu << 32;  // -inf, index -1
+__device__ __forceinline__ float value_of(Entry e) { return from_ordered((uint32_t)(e >> 32)); }
+__device__ __forceinline__ int index_of(Entry e) { return (int)~(uint32_t)e; }
+
+template <int D>
+__device__ __forceinline__ Entry entry_xor(Entry x) {
+  return (uint64_t)lane_xor<D>((uint32_t)(x >> 32)) << 32 | lane_xor<D>((uint32_t)x);
+}
+// Lane l and l ^ D in order: the larger to the lane with bit D clear, or set.
+template <int D>
+__device__ __forceinline__ Entry ordered_pair(Entry x, bool upper) {
+  const Entry o = entry_xor<D>(x);
+  return (o > x) != upper ? o : x;
+}
+// A list of any 64 entries, largest first.
+__device__ __forceinline__ Entry sorted(Entry x, int lane) {
+  x = ordered_pair<1>(x, (lane ^ lane >> 1) & 1);
+  auto stage = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    halving<N / 2>([&](auto d) {
+      constexpr int D = decltype(d)::value;
+      x = ordered_pair<D>(x, !(lane & D) != !(lane & N));
+    });
+  };
+  stage(std::integral_constant<int, 4>{});
+  stage(std::integral_constant<int, 8>{});
+  stage(std::integral_constant<int, 16>{});
+  stage(std::integral_constant<int, 32>{});
+  stage(std::integral_constant<int, 64>{});
+  return x;
+}
+// The largest 64 of two lists.
+__device__ __forceinline__ Entry joined(Entry x, Entry y, int lane) {
+  const Entry o = __shfl(y, 63 - lane);
+  if (o > x) x = o;
+  halving<32>([&](auto d) {
+    constexpr int D = decltype(d)::value;
+    x = ordered_pair<D>(x, lane & D);
+  });
+  return x;
 }
 // The largest float below the k-th largest of the lanes' (no NaN), or -inf.
 __device__ __forceinline__ float below_kth(float x, int k) {
@@ -149,10 +167,12 @@ template <int TYPE>
 __device__ __forceinline__ void load(const char *row, int V, int first, int lane, uint4 *out) {
   constexpr int PER = kPer<TYPE>, ES = 16 / PER;
 #pragma unroll
-  for (int i = 0; i < kLoads; i++) {
+  for (int i = 0; i < kLoads<TYPE>; i++) {
     const int at = first + (i * 64 + lane) * PER;
     if (at >= 0 && at <= V - PER) {
-      out[i] = *(const uint4 *)(row + (int64_t)at * ES);
+      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+      const u32x4 w = __builtin_nontemporal_load((const u32x4 *)(row + (int64_t)at * ES));  // (read once)
+      out[i] = uint4{w[0], w[1], w[2], w[3]};
     } else {
       uint32_t w[4];
 #pragma unroll
@@ -175,25 +195,34 @@ __device__ __forceinline__ void load(const char *row, int V, int first, int lane
 template <int TYPE, bool TOP>
 struct Wave {
   Sums sums;
-  List list;
-  float last;  // what a logit must be above to be looked at
+  Entry list;
+  float last;   // what a logit must be above to be collected
+  int waiting;  // collected: in LDS, fewer than 64 between runs
 
-  __device__ __forceinline__ void run(const uint4 *in, int first, float b2, int k, int lane, bool begin) {
-    constexpr int PER = kPer<TYPE>;
-    float x[kLoads][PER], most[kLoads];
+  // The 64 oldest that wait (or all) into the list.
+  __device__ __forceinline__ void take(Entry *wait, int lane) {
+    wave_sync();
+    const Entry x = lane < waiting ? wait[lane] : kNone, rest = wait[64 + lane];
+    wave_sync();
+    wait[lane] = rest;
+    waiting = max(waiting - 64, 0);
+    list = joined(list, sorted(x, lane), lane);
+  }
+
+  __device__ __forceinline__ void run(const uint4 *in, int first, float b2, int k, int lane, Entry *wait) {
+    constexpr int PER = kPer<TYPE>, LOADS = kLoads<TYPE>;
+    float x[LOADS][PER], most[LOADS], top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kLoads; i++) {
+    for (int i = 0; i < LOADS; i++) {
       unpack<TYPE>(in[i], x[i]);
-      most[i] = x[i][0];
+      most[i] = -INFINITY;
 #pragma unroll
-      for (int j = 1; j < PER; j++) most[i] = fmaxf(most[i], x[i][j]);
+      for (int j = 0; j < PER; j++) most[i] = fmaxf(most[i], x[i][j]);
+      top = fmaxf(top, most[i]);
     }
-    float top = most[0];
-#pragma unroll
-    for (int i = 1; i < kLoads; i++) top = fmaxf(top, most[i]);
     if (__ballot((top - sums.m) * b2 > 1.f)) sums.raise(fmaxf(sums.m, top), b2);
 #pragma unroll
-    for (int i = 0; i < kLoads; i++)
+    for (int i = 0; i < LOADS; i++)
 #pragma unroll
       for (int j = 0; j < PER; j++) {
         const float d = x[i][j] - sums.m, e = __builtin_amdgcn_exp2f(d * b2);
@@ -201,28 +230,43 @@ struct Wave {
         sums.q = fmaf(e, fmaxf(d, kLowest), sums.q);  // (0 times -inf is none)
       }
     if (!TOP) return;
-    if (begin) last = below_kth(top == top ? top : -INFINITY, k);
+    if (last == -INFINITY) last = below_kth(top, k);  // (fewer than k so far)
+    // (`last` stays as it is meanwhile: these are not in the order of their indices)
+    bool grown = false;
 #pragma unroll
-    for (int i = 0; i < kLoads; i++) {
-      uint64_t lanes = __ballot(most[i] > last);
-      while (lanes) {
-        const int l = __builtin_ctzll(lanes);
+    for (int i = 0; i < LOADS; i++) {
+      if (!__ballot(most[i] > last)) continue;
 #pragma unroll
-        for (int j = 0; j < PER; j++) {
-          const float v = of_lane(x[i][j], l) + 0.f;  // (no -0)
-          if (v > last) {
-            insert(list, v, first + (i * 64 + l) * PER + j, lane);
-            last = fmaxf(last, of_lane(list.v, k - 1));
-          }
+      for (int j = 0; j < PER; j++) {
+        const bool mine = x[i][j] > last;
+        const uint64_t lanes = __ballot(mine);
+        if (!lanes) continue;
+        const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0));
+        if (mine) wait[waiting + before] = entry_of(x[i][j], first + (i * 64 + lane) * PER + j);
+        waiting += (int)__popcll(lanes);
+        if (waiting >= 64) {
+          take(wait, lane);
+          grown = true;
         }
-        lanes = __ballot(most[i] > last) & ~((2ull << l) - 1);
       }
+    }
+    if (grown) {
+      const uint32_t kth = __builtin_amdgcn_readlane((uint32_t)(list >> 32), k - 1);
+      last = fmaxf(last, from_ordered(kth));
     }
   }
 };
 
+// The logit of the row's token (read long before it is used): -inf for one
+// that is none.
 template <int TYPE>
-__device__ void finish(const LogprobArgs &a, int t, Sums sums, List list, int lane) {
+__device__ __forceinline__ float logit_of(const LogprobArgs &a, int t) {
+  const int token = a.logprob ? a.tokens[t] : -1;
+  return token >= 0 && token < a.V ? value_at<TYPE>(a.logits, t * a.stride + token) : -INFINITY;
+}
+
+template <int TYPE>
+__device__ void finish(const LogprobArgs &a, int t, float logit, Sums sums, Entry list, int lane) {
   const char *row = (const char *)a.logits + t * a.stride * (16 / kPer<TYPE>);
   const float log2_s = log2f(sums.s);
   auto log_p = [&](float x) {  // S = 0: no logit above -inf
@@ -231,7 +275,7 @@ __device__ void finish(const LogprobArgs &a, int t, Sums sums, List list, int la
   if (lane == 0) {
     if (a.logprob) {
       const int token = a.tokens[t];
-      a.logprob[t] = token >= 0 && token < a.V ? log_p(value_at<TYPE>(row, token)) : -INFINITY;
+      a.logprob[t] = token >= 0 && token < a.V ? log_p(logit) : -INFINITY;
     }
     if (a.entropy) {
       const float h = sums.s == 0.f ? 0.f : log2_s * kLn2 - a.beta * (sums.q / sums.s);
@@ -240,33 +284,34 @@ __device__ void finish(const LogprobArgs &a, int t, Sums sums, List list, int la
     if (a.lse) a.lse[t] = sums.s == 0.f ? -INFINITY : fmaf(sums.m, a.beta, log2_s * kLn2);
   }
   if (!a.k) return;
+  float v = value_of(list);
+  int at = index_of(list);
   // fewer than k logits above -inf: the first of those that are -inf
-  int found = __popcll(__ballot(list.at != 0x7fffffff));
+  int found = (int)__popcll(__ballot(at >= 0));
   if (found < a.k) {
     for (int x0 = 0; x0 < a.V && found < a.k; x0 += 64) {
       const int x = x0 + lane;
       const uint64_t there = __ballot(x < a.V && value_at<TYPE>(row, min(x, a.V - 1)) == -INFINITY);
-      const int n = __popcll(there);
+      const int n = (int)__popcll(there);
       if (lane >= found && lane < found + n) {
         uint64_t rest = there;  // its (lane - found)-th
         for (int i = found; i < lane; i++) rest &= rest - 1;
-        list.at = x0 + __builtin_ctzll(rest);
+        at = x0 + __builtin_ctzll(rest);
       }
       found += n;
     }
   }
   if (lane < a.k) {
-    const bool none = list.at == 0x7fffffff;  // the others are NaN
-    a.top[(int64_t)t * a.k + lane] = none ? -1 : list.at;
-    a.top_logprob[(int64_t)t * a.k + lane] = none ? NAN : log_p(list.v);
+    a.top[(int64_t)t * a.k + lane] = at;
+    a.top_logprob[(int64_t)t * a.k + lane] = at < 0 ? NAN : log_p(v);  // (the others are NaN)
   }
 }
 
 template <int TYPE, bool TOP>
-__global__ __launch_bounds__(kThreads) void token_logprobs_kernel(LogprobArgs a) {
+__global__ __launch_bounds__(kThreads, 8) void token_logprobs_kernel(LogprobArgs a) {
   __shared__ Sums sums[kWaves];
-  __shared__ List lists[kWaves][64];
-  constexpr int RUN = kRun<TYPE>;
+  __shared__ Entry lists[TOP ? kWaves : 1][128];
+  constexpr int RUN = kRun;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int t = blockIdx.x / a.parts, part = blockIdx.x - t * a.parts;
   const char *row = (const char *)a.logits + t * a.stride * (16 / kPer<TYPE>);
@@ -274,26 +319,28 @@ __global__ __launch_bounds__(kThreads) void token_logprobs_kernel(LogprobArgs a)
   const int lead = (int)((uintptr_t)row % 16) / (16 / kPer<TYPE>);
   const int runs = (a.V + lead + RUN - 1) / RUN;
   const int lo = (int)((int64_t)runs * part / a.parts), hi = (int)((int64_t)runs * (part + 1) / a.parts);
-  const float b2 = a.beta * kLog2e;
+  const float b2 = a.beta * kLog2e, logit = a.parts == 1 ? logit_of<TYPE>(a, t) : 0.f;
   Wave<TYPE, TOP> w;
   w.sums = Sums{kLowest, 0.f, 0.f};
-  w.list = List{-INFINITY, 0x7fffffff};
+  w.list = kNone;
   w.last = -INFINITY;
-  uint4 next[kLoads];
+  w.waiting = 0;
+  uint4 next[kLoads<TYPE>];
   int x = lo + wave;
   if (x < hi) load<TYPE>(row, a.V, x * RUN - lead, lane, next);
   for (; x < hi; x += kWaves) {
-    uint4 now[kLoads];
+    uint4 now[kLoads<TYPE>];
 #pragma unroll
-    for (int i = 0; i < kLoads; i++) now[i] = next[i];
+    for (int i = 0; i < kLoads<TYPE>; i++) now[i] = next[i];
     if (x + kWaves < hi) load<TYPE>(row, a.V, (x + kWaves) * RUN - lead, lane, next);
-    w.run(now, x * RUN - lead, b2, a.k, lane, x == lo + wave);
+    w.run(now, x * RUN - lead, b2, a.k, lane, lists[TOP ? wave : 0]);
   }
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2)
-    w.sums.join(Sums{__shfl_xor(w.sums.m, d), __shfl_xor(w.sums.s, d), __shfl_xor(w.sums.q, d)}, b2);
+  w.sums.join_lanes(b2);
   if (lane == 0) sums[wave] = w.sums;
-  if (TOP) lists[wave][lane] = w.list;
+  if (TOP) {
+    w.take(lists[wave], lane);
+    lists[wave][lane] = w.list;
+  }
   __syncthreads();
   if (wave) return;
 #pragma unroll
@@ -301,35 +348,30 @@ __global__ __launch_bounds__(kThreads) void token_logprobs_kernel(LogprobArgs a)
     w.sums.join(sums[i], b2);
     if (TOP) w.list = joined(w.list, lists[i][lane], lane);
   }
-  if (a.parts == 1) return finish<TYPE>(a, t, w.sums, w.list, lane);
+  if (a.parts == 1) return finish<TYPE>(a, t, logit, w.sums, w.list, lane);
   float *out = a.part + (int64_t)blockIdx.x * (4 + 2 * a.k);
   if (lane == 0) {
     out[0] = w.sums.m;
     out[1] = w.sums.s;
     out[2] = w.sums.q;
   }
-  if (TOP && lane < a.k) {
-    out[4 + lane] = w.list.v;
-    ((int *)out)[4 + a.k + lane] = w.list.at;
-  }
+  if (TOP && lane < a.k) ((Entry *)(out + 4))[lane] = w.list;
 }
 
 // Joins a row's parts: their lists' entries go to the lanes of all waves, each
 // wave sorts its 64, and the waves' lists join in pairs.
 template <int TYPE>
 __global__ __launch_bounds__(64 * kJoinWaves) void join_logprobs_kernel(LogprobArgs a) {
-  __shared__ List lists[kJoinWaves][64];
+  __shared__ Entry lists[kJoinWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.x;
-  const float b2 = a.beta * kLog2e;
+  const float b2 = a.beta * kLog2e, logit = logit_of<TYPE>(a, t);
   const size_t words = 4 + 2 * a.k;
   const float *in = a.part + (size_t)t * a.parts * words;
   const int entries = a.parts * a.k, used = min(kJoinWaves, (entries + 63) / 64);
-  List list = {-INFINITY, 0x7fffffff};
+  Entry list = kNone;
   for (int x0 = 64 * wave; x0 < entries; x0 += 64 * kJoinWaves) {
     const int x = x0 + lane, p = x / max(a.k, 1), j = x - p * a.k;
-    List o = {-INFINITY, 0x7fffffff};
-    if (x < entries) o = List{in[p * words + 4 + j], ((const int *)in)[p * words + 4 + a.k + j]};
-    o = sorted(o, lane);
+    const Entry o = sorted(x < entries ? ((const Entry *)(in + p * words + 4))[j] : kNone, lane);
     list = x0 < 64 * kJoinWaves ? o : joined(list, o, lane);
   }
   for (int d = 1; d < used; d *= 2) {
@@ -340,10 +382,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_logprobs_kernel(LogprobA
   if (wave) return;
   Sums sums = {kLowest, 0.f, 0.f};
   for (int p = lane; p < a.parts; p += 64) sums.join(Sums{in[p * words], in[p * words + 1], in[p * words + 2]}, b2);
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2)
-    sums.join(Sums{__shfl_xor(sums.m, d), __shfl_xor(sums.s, d), __shfl_xor(sums.q, d)}, b2);
-  finish<TYPE>(a, t, sums, list, lane);
+  sums.join_lanes(b2);
+  finish<TYPE>(a, t, logit, sums, list, lane);
 }
 
 template <int TYPE>
@@ -360,11 +400,15 @@ hipError_t launch(const LogprobArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Parts of a row: so many that the card is full, and each wave of a part has a
-// run of 16-bit logits.
+// Parts of a row: so many that four workgroups are there for each CU, and each
+// wave of a part has a run. Every wave has a list of its own to begin and to
+// join, so that more of them cost more than they hide: 1000 rows of 150001 fp32
+// logits with 20 alternatives take 102 us in one part (four to a CU), 113 in two,
+// 122 in four; one row of 131072, for which only latency counts, 10.7 us in 32
+// parts, 11.4 in 16 and 13.4 in 8.
 int logprob_parts(int T, int V) {
-  const int most = std::max(1, V / (kWaves * kRun<K3_BF16>));
-  return std::max(1, std::min(most, 8 * num_cus() / std::max(T, 1)));
+  const int most = std::max(1, V / (kWaves * kRun));
+  return std::max(1, std::min(most, 4 * num_cus() / std::max(T, 1)));
 }
 
 hipError_t launch_token_logprobs(const LogprobArgs &a, hipStream_t s) {
