@@ -20,7 +20,9 @@
 // its first row's window on are taken: they are numbered without the gap, as
 // if the request were so much shorter (its rows' positions and windows with
 // it; what is below the gap is seen by the sinks' rule alone), and
-// real_place() turns such a place into the cache's.
+// real_place() turns such a place into the cache's. Tiles are short then, and
+// often alike: where that takes less time, workgroups get whole tiles (each
+// counts as one unit of the line), and nothing is joined.
 #pragma once
 
 #include <math.h>
@@ -86,14 +88,15 @@ __device__ __forceinline__ int node_of(const AttnArgs &a, int row) {
 // fixed, the first tile's places, what each next one has more. The last one's
 // places count for less if it is of up to HALF rows. T * Hq <= 2^30 rows and
 // 2^30 places keep all sums below 2^61.
-// With a window a tile has at most `cap`: tiles from `capped` on.
+// With a window a tile has at most `cap`: tiles from `capped` on. unit: what a
+// tile counts if they go whole (0: they do not).
 template <int RT, int HALF, bool WIN>
 struct Cost {
   int tiles, last_rows;
   long long base, slope, all;
-  long long cap, capped;  // WIN
+  long long cap, capped, unit;  // WIN
   static constexpr long long kFixed = 16 * kFixedPlaces<RT>;
-  __device__ __forceinline__ Cost(const AttnArgs &a, const Request &q) {
+  __device__ __forceinline__ Cost(const AttnArgs &a, const Request &q, long long unit = 0) : unit(unit) {
     const long long rows = (long long)q.n * a.G;
     tiles = (int)((rows + RT - 1) / RT);
     last_rows = (int)(rows - (long long)(tiles - 1) * RT);
@@ -112,12 +115,14 @@ struct Cost {
   __device__ __forceinline__ int weight(int x) const { return x == tiles - 1 && last_rows <= HALF ? kHalfCost : 16; }
   __device__ __forceinline__ long long of_first(long long x) const {
     if constexpr (WIN) {
+      if (unit) return x * unit;
       const long long y = min(x, capped);
       return x * kFixed + y * base + slope * (y * (y - 1) / 2) + (x - y) * cap;
     }
     return x * (kFixed + base) + slope * (x * (x - 1) / 2);
   }
   __device__ __forceinline__ long long of(int x) const {
+    if (WIN && unit) return unit;
     const long long places = WIN && x >= capped ? cap : base + slope * x;
     return kFixed + (places * weight(x) >> 4);
   }
@@ -130,33 +135,73 @@ struct Cost {
 template <int THREADS>
 struct Line {
   long long pre[THREADS + 1], wave_sum[THREADS / 64];
+  int wave_tiles[THREADS / 64], wave_most[THREADS / 64];  // WIN
   Request request[THREADS];  // the last of each thread's
 };
 template <int THREADS>
 __device__ __forceinline__ int run_of(int R) { return (R + THREADS - 1) / THREADS; }
 
+// Returns what a tile counts if they go whole, else 0. They do if the most that
+// a workgroup has then takes no longer than an equal stretch and what two parts of
+// tiles cost more than whole ones (a tile's fixed cost, and about as much for the
+// parts' way through memory and the joining launch).
+constexpr int kUnit = 16;
 template <int RT, int HALF, bool WIN, int THREADS>
-__device__ __forceinline__ void line_of_tiles(const AttnArgs &a, Line<THREADS> &L) {
+__device__ __forceinline__ long long line_of_tiles(const AttnArgs &a, Line<THREADS> &L) {
   const int tid = threadIdx.x, lane = tid & 63, per = run_of<THREADS>(a.R);
   long long own = 0;
+  int own_tiles = 0, most = 0;  // (T * Hq <= 2^30 rows, 2^5 cost of a row at least)
   for (int r = tid * per; r < min(a.R, tid * per + per); r++) {
     const Request q = request_of(a, r);
-    own += Cost<RT, HALF, WIN>(a, q).of_request(a);
+    const Cost<RT, HALF, WIN> cost(a, q);
+    own += cost.of_request(a);
     L.request[tid] = q;
+    if constexpr (WIN) {
+      own_tiles += cost.tiles * a.c.n_heads;
+      const long long longest = cost.tiles ? max(cost.of(cost.tiles - 1), cost.of(max(cost.tiles - 2, 0))) : 0;
+      most = max(most, (int)min(longest >> 4, (long long)INT32_MAX));
+    }
   }
   long long incl = own;
+  int tiles = own_tiles;
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) {
     const long long x = __shfl_up(incl, m);
     if (lane >= m) incl += x;
+    if constexpr (WIN) {
+      const int t = __shfl_up(tiles, m);
+      if (lane >= m) tiles += t;
+      most = max(most, __shfl_xor(most, m));
+    }
   }
   if (lane == 63) L.wave_sum[tid >> 6] = incl;
+  if (WIN && lane == 63) {
+    L.wave_tiles[tid >> 6] = tiles;
+    L.wave_most[tid >> 6] = most;
+  }
   __syncthreads();
-  long long base = incl - own;
+  long long base = incl - own, unit = 0;
   for (int w = 0; w < (tid >> 6); w++) base += L.wave_sum[w];
+  if constexpr (WIN) {
+    long long all = 0;
+    int all_tiles = 0, before = tiles - own_tiles;
+    for (int w = 0; w < THREADS / 64; w++) {
+      all += L.wave_sum[w];
+      if (w < (tid >> 6)) before += L.wave_tiles[w];
+      all_tiles += L.wave_tiles[w];
+      most = max(most, L.wave_most[w]);
+    }
+    const int rounds = (int)ceil((double)all_tiles * a.inv_groups);
+    if ((double)rounds * most <= (double)all / 16 * a.inv_groups + 2 * kFixedPlaces<RT>) {
+      unit = kUnit;
+      base = (long long)kUnit * before;
+      own = (long long)kUnit * own_tiles;
+    }
+  }
   L.pre[tid] = base;
   if (tid == THREADS - 1) L.pre[THREADS] = base + own;
   __syncthreads();
+  return unit;
 }
 
 // Values that are the same in all lanes, as such.
@@ -220,7 +265,7 @@ __device__ __forceinline__ void fill_tile(const AttnArgs &a, Tile &t, const Cost
 }
 // The tile that place u of the line is in.
 template <int RT, int KB, int HALF, bool WIN, int THREADS>
-__device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &L, long long u) {
+__device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &L, long long unit, long long u) {
   Tile t;
   // the last thread whose requests begin at or before it, and its request
   const int per = run_of<THREADS>(a.R);
@@ -234,12 +279,12 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &
   t.r = run * per;
   t.q = request_again(a, L, t.r);
   for (; t.r + 1 < min(a.R, run * per + per); t.r++) {
-    const long long all = Cost<RT, HALF, WIN>(a, t.q).of_request(a);
+    const long long all = Cost<RT, HALF, WIN>(a, t.q, unit).of_request(a);
     if (before + all > u) break;
     before += all;
     t.q = request_again(a, L, t.r + 1);
   }
-  const Cost<RT, HALF, WIN> cost(a, t.q);
+  const Cost<RT, HALF, WIN> cost(a, t.q, unit);
   // (the product is off by less than 1: n_heads <= 2^10)
   t.h = (int)((double)(u - before) * __builtin_amdgcn_rcp((double)cost.all));
   t.h = min(max(t.h, 0), a.c.n_heads - 1);
@@ -259,7 +304,7 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &
 }
 // The next tile (there is one).
 template <int RT, int KB, int HALF, bool WIN, int THREADS>
-__device__ __forceinline__ void next_tile(const AttnArgs &a, const Line<THREADS> &L, Tile &t) {
+__device__ __forceinline__ void next_tile(const AttnArgs &a, const Line<THREADS> &L, long long unit, Tile &t) {
   t.first = t.after;
   if (++t.x == t.tiles) {
     t.x = 0;
@@ -269,7 +314,7 @@ __device__ __forceinline__ void next_tile(const AttnArgs &a, const Line<THREADS>
       while (t.q.n == 0 && t.r + 1 < a.R);
     }
   }
-  fill_tile<RT, KB, HALF, WIN>(a, t, Cost<RT, HALF, WIN>(a, t.q));
+  fill_tile<RT, KB, HALF, WIN>(a, t, Cost<RT, HALF, WIN>(a, t.q, unit));
 }
 
 // The same in scalar registers: what was worked out in fp64 is in vector ones
@@ -295,12 +340,17 @@ __device__ __forceinline__ int block_from(const Tile &t, long long u) {
 }
 
 // Where workgroup b's stretch of the line begins: equal ones, the last a
-// little shorter.
+// little shorter. Whole tiles: as equal as they can be.
 struct Stretches {
-  long long cost, each;
-  __device__ __forceinline__ Stretches(const AttnArgs &a, long long cost)
-      : cost(cost), each((long long)((double)cost * a.inv_groups) + (cost >> 50) + 1) {}
-  __device__ __forceinline__ long long begin(int b) const { return min(cost, each * b); }
+  long long cost, each, unit;
+  double groups;  // 1 / them
+  __device__ __forceinline__ Stretches(const AttnArgs &a, long long cost, long long unit)
+      : cost(cost), each((long long)((double)cost * a.inv_groups) + (cost >> 50) + 1), unit(unit), groups(a.inv_groups) {}
+  __device__ __forceinline__ long long begin(int b) const {
+    // (the half keeps the quotient off whole numbers, where it is rounded either way)
+    if (unit) return (long long)(((double)(cost / kUnit) * b + 0.5) * groups) * kUnit;
+    return min(cost, each * b);
+  }
 };
 // Neighbours in the line read the same keys: they go to one die (workgroups
 // go to the eight dies in turn, and each has an L2 of its own).
@@ -336,15 +386,16 @@ __device__ __forceinline__ JoinJob *join_jobs(const AttnArgs &a, int B) {
 template <int RT, int KB, int HALF, bool WIN, int D, int THREADS, class Segment>
 __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
   __shared__ Line<THREADS> L;
-  line_of_tiles<RT, HALF, WIN, THREADS>(a, L);
+  long long unit = line_of_tiles<RT, HALF, WIN, THREADS>(a, L);
+  unit = WIN ? in_all_lanes(unit) : 0;
   const int B = gridDim.x, b = place_in_line(blockIdx.x, B);
-  const Stretches line(a, in_all_lanes(L.pre[THREADS]));
+  const Stretches line(a, in_all_lanes(L.pre[THREADS]), unit);
   const long long begin = line.begin(b), end = line.begin(b + 1);
   JoinJob job = {0, 0, 0, 0, -1, -1, -1, 0};
   Tile tile;
   for (long long u = begin; u < end;) {
-    if (u == begin) tile = tile_at<RT, KB, HALF, WIN>(a, L, u);
-    else next_tile<RT, KB, HALF, WIN>(a, L, tile);
+    if (u == begin) tile = tile_at<RT, KB, HALF, WIN>(a, L, unit, u);
+    else next_tile<RT, KB, HALF, WIN>(a, L, unit, tile);
     if constexpr (WIN) to_scalars(tile);
     const int lo = block_from<RT, KB>(tile, u), hi = block_from<RT, KB>(tile, end);
     const int slot = lo == hi || (lo == 0 && hi == tile.blocks) ? -1 : lo ? 2 * b : 2 * b + 1;
