@@ -16,8 +16,8 @@
 // within each.
 //
 // Windows. A row at position x sees the places below `sinks` and those above
-// x - window. Of a tile's places only the blocks up to the sinks' end and from
-// its first row's window on are taken: they are numbered without the gap, as
+// x - window. Of a tile's places only those up to the sinks' end and from its
+// first row's window on are taken, in runs of 32: they are numbered without the gap, as
 // if the request were so much shorter (its rows' positions and windows with
 // it; what is below the gap is seen by the sinks' rule alone), and
 // real_place() turns such a place into the cache's. Tiles are short then, and
@@ -141,11 +141,17 @@ struct Line {
 template <int THREADS>
 __device__ __forceinline__ int run_of(int R) { return (R + THREADS - 1) / THREADS; }
 
-// Returns what a tile counts if they go whole, else 0. They do if the most that
-// a workgroup has then takes no longer than an equal stretch and what two parts of
+// What a tile counts if they go whole, else 0. They do if the most that a
+// workgroup has then takes no longer than an equal stretch and what two parts of
 // tiles cost more than whole ones (a tile's fixed cost, and about as much for the
-// parts' way through memory and the joining launch).
+// parts' way through memory and the joining launch). all: in sixteenths of a
+// place; most: the longest tile in places.
 constexpr int kUnit = 16;
+template <int RT>
+__device__ __forceinline__ long long unit_of(const AttnArgs &a, long long all, int tiles, int most) {
+  const int rounds = (int)ceil((double)tiles * a.inv_groups);
+  return (double)rounds * most <= (double)all / 16 * a.inv_groups + 2 * kFixedPlaces<RT> ? kUnit : 0;
+}
 template <int RT, int HALF, bool WIN, int THREADS>
 __device__ __forceinline__ long long line_of_tiles(const AttnArgs &a, Line<THREADS> &L) {
   const int tid = threadIdx.x, lane = tid & 63, per = run_of<THREADS>(a.R);
@@ -191,9 +197,8 @@ __device__ __forceinline__ long long line_of_tiles(const AttnArgs &a, Line<THREA
       all_tiles += L.wave_tiles[w];
       most = max(most, L.wave_most[w]);
     }
-    const int rounds = (int)ceil((double)all_tiles * a.inv_groups);
-    if ((double)rounds * most <= (double)all / 16 * a.inv_groups + 2 * kFixedPlaces<RT>) {
-      unit = kUnit;
+    unit = unit_of<RT>(a, all, all_tiles, most);
+    if (unit) {
       base = (long long)kUnit * before;
       own = (long long)kUnit * own_tiles;
     }
@@ -228,19 +233,34 @@ struct Tile {
   int weight;              // Cost::weight
   long long first, after;  // its stretch of the line
   int tiles;               // of its key head
-  // WIN: blocks of the sinks, blocks that are left out behind them, the first
-  // place (without the gap) that is in the window of all rows
-  int sink_blocks, skipped, near;
+  // WIN: places of the sinks' runs, those that are left out behind them, the
+  // first place (without the gap) that is in the window of all rows
+  int sinks, skipped, near;
 };
 // Place y of a tile's, counted without the gap, in the cache; and the request
 // as it is without the gap.
-template <bool WIN, int KB>
+template <bool WIN>
 __device__ __forceinline__ int real_place(const Tile &t, int y) {
-  return WIN && y >= t.sink_blocks * KB ? y + t.skipped * KB : y;
+  return WIN && y >= t.sinks ? y + t.skipped : y;
 }
-template <bool WIN, int KB>
+template <bool WIN>
 __device__ __forceinline__ Request without_gap(const Tile &t) {
-  return {t.q.t0, t.q.n, t.q.len - (WIN ? t.skipped * KB : 0)};
+  return {t.q.t0, t.q.n, t.q.len - (WIN ? t.skipped : 0)};
+}
+// What a tile's rows see, from q, row0 and rows.
+template <int KB, bool WIN>
+__device__ __forceinline__ void fill_places(const AttnArgs &a, Tile &t) {
+  t.places = t.q.len;
+  if (!a.mask) t.places = min(t.q.len, max(0, t.q.len - t.q.n + node_of(a, t.row0 + t.rows - 1) + 1));
+  if constexpr (WIN) {
+    // (a tree's row is at its request's last committed place or later)
+    const int ctx = t.q.len - t.q.n, first = a.mask ? ctx - 1 : ctx + node_of(a, t.row0);
+    t.sinks = (min(a.sinks, max(t.places, 0)) + 31) & -32;
+    t.skipped = max(0, (min(max(0, first - a.window + 1), max(t.places - 1, 0)) & -32) - t.sinks);
+    t.places -= t.skipped;
+    t.near = t.places - a.window;
+  }
+  t.blocks = t.places > 0 ? (t.places - 1) / KB + 1 : 1;
 }
 // The rest of a tile from q, r, h, x and first.
 template <int RT, int KB, int HALF, bool WIN>
@@ -250,18 +270,7 @@ __device__ __forceinline__ void fill_tile(const AttnArgs &a, Tile &t, const Cost
   t.rows = t.x == cost.tiles - 1 ? cost.last_rows : RT;
   t.weight = cost.weight(t.x);
   t.after = t.first + cost.of(t.x);
-  t.places = t.q.len;
-  if (!a.mask) t.places = min(t.q.len, max(0, t.q.len - t.q.n + node_of(a, t.row0 + t.rows - 1) + 1));
-  t.blocks = t.places > 0 ? (t.places - 1) / KB + 1 : 1;
-  if constexpr (WIN) {
-    // (a tree's row is at its request's last committed place or later)
-    const int ctx = t.q.len - t.q.n, first = a.mask ? ctx - 1 : ctx + node_of(a, t.row0);
-    t.sink_blocks = (min(a.sinks, max(t.places, 0)) + KB - 1) / KB;
-    t.skipped = max(0, min(max(0, first - a.window + 1) / KB, t.blocks - 1) - t.sink_blocks);
-    t.blocks -= t.skipped;
-    t.places -= t.skipped * KB;
-    t.near = t.places - a.window;
-  }
+  fill_places<KB, WIN>(a, t);
 }
 // The tile that place u of the line is in.
 template <int RT, int KB, int HALF, bool WIN, int THREADS>
@@ -321,7 +330,7 @@ __device__ __forceinline__ void next_tile(const AttnArgs &a, const Line<THREADS>
 // otherwise, of which the walk holds more than it has with a window.
 __device__ __forceinline__ void to_scalars(Tile &t) {
   for (int *x : {&t.q.t0, &t.q.n, &t.q.len, &t.r, &t.h, &t.x, &t.row0, &t.rows, &t.places, &t.blocks, &t.weight,
-                 &t.tiles, &t.sink_blocks, &t.skipped, &t.near})
+                 &t.tiles, &t.sinks, &t.skipped, &t.near})
     *x = __builtin_amdgcn_readfirstlane(*x);
   t.first = in_all_lanes(t.first);
   t.after = in_all_lanes(t.after);
@@ -337,6 +346,102 @@ __device__ __forceinline__ int block_from(const Tile &t, long long u) {
   long long y = max(u - t.first - 16 * kFixedPlaces<RT>, 0ll);
   if (t.weight != 16) y = y * 93 >> 6;  // 16 / 11
   return (int)min((y + 16 * KB - 1) / (16 * KB), (long long)t.blocks);
+}
+
+// The same line where every request is one tile of each key head, which most
+// calls of the streaming kernel have: a quarter of the way's instructions (each
+// 128 bytes of them are fetched anew by every launch, and take longer than they
+// run: one place for each of 64 requests XX -> XX us). Says whether they are.
+template <int RT, int KB>
+__device__ __forceinline__ long long short_cost(const Tile &t) {
+  return t.rows ? 16ll * (kFixedPlaces<RT> + t.places) : 0;
+}
+__device__ __forceinline__ void as_one_tile(const AttnArgs &a, Tile &t) {
+  t.x = t.row0 = 0;
+  t.rows = t.q.n * a.G;
+  t.weight = 16;
+  t.tiles = 1;
+}
+template <int RT, int KB, int THREADS>
+__device__ __forceinline__ bool short_line(const AttnArgs &a, Line<THREADS> &L, long long &unit) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  Tile t;
+  t.q = {0, 0, 0};
+  if (tid < a.R) t.q = request_of(a, tid);
+  as_one_tile(a, t);
+  fill_places<KB, true>(a, t);
+  const bool one = t.rows <= RT;
+  const uint64_t here = __ballot(t.rows > 0);
+  const long long own = short_cost<RT, KB>(t) * a.c.n_heads;
+  long long incl = own;
+  int most = t.rows ? kFixedPlaces<RT> + t.places : 0;
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) {
+    const long long x = __shfl_up(incl, m);
+    if (lane >= m) incl += x;
+    most = max(most, __shfl_xor(most, m));
+  }
+  L.request[tid] = t.q;
+  if (lane == 63) {
+    L.wave_sum[wave] = incl;
+    L.wave_tiles[wave] = __popcll(here);
+    L.wave_most[wave] = most;
+  }
+  if (!__syncthreads_and(one)) return false;
+  long long all = 0, base = incl - own;
+  int tiles = 0, before = __popcll(here & ((1ull << lane) - 1));
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; w++) {
+    if (w < wave) {
+      base += L.wave_sum[w];
+      before += L.wave_tiles[w];
+    }
+    all += L.wave_sum[w];
+    tiles += L.wave_tiles[w];
+    most = max(most, L.wave_most[w]);
+  }
+  unit = unit_of<RT>(a, all, tiles * a.c.n_heads, most);
+  if (unit) {
+    base = (long long)(kUnit * a.c.n_heads) * before;
+    all = (long long)(kUnit * a.c.n_heads) * tiles;
+  }
+  L.pre[tid] = base;
+  if (tid == 0) L.pre[THREADS] = all;
+  __syncthreads();
+  return true;
+}
+// The tile that place u of it is in, and the next one.
+template <int RT, int KB, int THREADS>
+__device__ __forceinline__ Tile short_tile_at(const AttnArgs &a, const Line<THREADS> &L, long long unit, long long u) {
+  Tile t;
+  int r = 0;  // requests that end at or before it
+#pragma unroll
+  for (int w = 0; w < THREADS; w += 64) r += __popcll(__ballot(L.pre[w + 1 + (threadIdx.x & 63)] <= u));
+  t.r = r;
+  t.q = request_again(a, L, r);
+  as_one_tile(a, t);
+  fill_places<KB, true>(a, t);
+  const long long cost = unit ? unit : short_cost<RT, KB>(t), head = in_all_lanes(L.pre[r]);
+  // (a quotient below 2^10, off by less than 1)
+  t.h = (int)((float)(u - head) / (float)cost);
+  t.h = min(max(t.h, 0), a.c.n_heads - 1);
+  if (t.h * cost > u - head) t.h--;
+  else if ((t.h + 1) * cost <= u - head) t.h++;
+  t.first = head + t.h * cost;
+  t.after = t.first + cost;
+  return t;
+}
+template <int RT, int KB, int THREADS>
+__device__ __forceinline__ void short_next_tile(const AttnArgs &a, const Line<THREADS> &L, long long unit, Tile &t) {
+  if (++t.h == a.c.n_heads) {
+    t.h = 0;
+    do t.q = request_again(a, L, ++t.r);
+    while (t.q.n == 0 && t.r + 1 < a.R);
+    as_one_tile(a, t);
+    fill_places<KB, true>(a, t);
+  }
+  t.first = t.after;
+  t.after += unit ? unit : short_cost<RT, KB>(t);
 }
 
 // Where workgroup b's stretch of the line begins: equal ones, the last a
@@ -383,10 +488,14 @@ __device__ __forceinline__ JoinJob *join_jobs(const AttnArgs &a, int B) {
 
 // The walk of a workgroup over its stretch of the line, with
 // segment(tile, first block, block after the last, slot or -1).
-template <int RT, int KB, int HALF, bool WIN, int D, int THREADS, class Segment>
+// SHORT: with the way of its own for requests of one tile.
+template <int RT, int KB, int HALF, bool WIN, bool SHORT, int D, int THREADS, class Segment>
 __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
   __shared__ Line<THREADS> L;
-  long long unit = line_of_tiles<RT, HALF, WIN, THREADS>(a, L);
+  long long unit = 0;
+  bool brief = false;
+  if constexpr (SHORT) brief = a.R <= THREADS && short_line<RT, KB>(a, L, unit);
+  if (!brief) unit = line_of_tiles<RT, HALF, WIN, THREADS>(a, L);
   unit = WIN ? in_all_lanes(unit) : 0;
   const int B = gridDim.x, b = place_in_line(blockIdx.x, B);
   const Stretches line(a, in_all_lanes(L.pre[THREADS]), unit);
@@ -394,7 +503,10 @@ __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
   JoinJob job = {0, 0, 0, 0, -1, -1, -1, 0};
   Tile tile;
   for (long long u = begin; u < end;) {
-    if (u == begin) tile = tile_at<RT, KB, HALF, WIN>(a, L, unit, u);
+    if (SHORT && brief) {
+      if (u == begin) tile = short_tile_at<RT, KB>(a, L, unit, u);
+      else short_next_tile<RT, KB>(a, L, unit, tile);
+    } else if (u == begin) tile = tile_at<RT, KB, HALF, WIN>(a, L, unit, u);
     else next_tile<RT, KB, HALF, WIN>(a, L, unit, tile);
     if constexpr (WIN) to_scalars(tile);
     const int lo = block_from<RT, KB>(tile, u), hi = block_from<RT, KB>(tile, end);

@@ -78,11 +78,10 @@ struct Stream {
     return b < (uint32_t)a.blocks ? row[b] : -1;
   }
 
-  // The places from k0 on: this lane's (lane % PLACES) page is `page`. Leaves
-  // the rows' offsets in LDS; places that are not there read row 0.
-  static __device__ __forceinline__ void places(const AttnArgs &a, Wave &w, int64_t *offset, int lane, int h, int k0,
+  // A wave's next places: this lane's (lane % PLACES) is p, in the page `page`.
+  // Leaves the rows' offsets in LDS; places that are not there read row 0.
+  static __device__ __forceinline__ void places(const AttnArgs &a, Wave &w, int64_t *offset, int lane, int h, int p,
                                                 int page) {
-    const int p = k0 + lane % PLACES;
     const bool there = page >= 0 && page < a.c.n_pages;
     const uint32_t b = __umulhi(2u * (uint32_t)p, a.page_magic) >> a.page_shift;
     const int64_t at = page * a.c.page_stride + (int)((uint32_t)p - b * a.c.page_size) * a.c.slot_stride;
@@ -351,7 +350,7 @@ struct Stream {
   static __device__ __forceinline__ void segment(const AttnArgs &a, Lds &L, const Tile &tile, int lo, int hi,
                                                  int slot, int B) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
-    const Request shorter = without_gap<WIN, KB>(tile), &rq = WIN ? shorter : tile.q;
+    const Request shorter = without_gap<WIN>(tile), &rq = WIN ? shorter : tile.q;
     const int rows = rq.n * a.G;
     Wave w;
     int node[QT], near[QT];
@@ -376,13 +375,13 @@ struct Stream {
     const int32_t *table = a.table + (size_t)tile.r * a.blocks;
     int64_t *offset = L.offset[wave];
     const int end = (int)min((long long)hi * KB, (long long)tile.places);
-    auto real = [&](int y) { return real_place<WIN, KB>(tile, y); };  // (a wave's places are in one block)
+    auto place = [&](int y) { return real_place<WIN>(tile, y + lane % PLACES); };  // the lane's of those from y on
     int k0 = lo * KB + PLACES * wave;
-    int page = table_entry(a, table, real(k0) + lane % PLACES, tile.q.len);
+    int page = table_entry(a, table, place(k0), tile.q.len);
     if (k0 < end) {
-      places(a, w, offset, lane, tile.h, real(k0), page);
+      places(a, w, offset, lane, tile.h, place(k0), page);
       load(w, k, v, offset, c, g);
-      page = table_entry(a, table, real(k0 + KB) + lane % PLACES, tile.q.len);
+      page = table_entry(a, table, place(k0 + KB), tile.q.len);
       for (; k0 < end; k0 += KB) {
         if constexpr (BLK) {
           if (lane < PLACES) {
@@ -396,8 +395,8 @@ struct Stream {
           run<RUNS - 1>(a, w, rq, tile.near, node, near, k0 + 32, scale, v, offset + PLACES - 32, L.power[wave],
                         L.o[wave], c, g);
         if (k0 + KB < end) {
-          places(a, w, offset, lane, tile.h, real(k0 + KB), page);
-          page = table_entry(a, table, real(k0 + 2 * KB) + lane % PLACES, tile.q.len);
+          places(a, w, offset, lane, tile.h, place(k0 + KB), page);
+          page = table_entry(a, table, place(k0 + 2 * KB), tile.q.len);
           load(w, k, v, offset, c, g);
         }
       }
@@ -478,7 +477,7 @@ template <bool BF, bool F8, int D, int QT, int MODE>
 __global__ __launch_bounds__(kStreamThreads, (kStreamFit<D, QT, MODE>)) void attn_stream_kernel(AttnArgs a) {
   using S = Stream<BF, F8, D, QT, MODE>;
   __shared__ typename S::Lds L;
-  walk<S::RT, S::KB, 0, S::WIN, D, kStreamThreads>(a, [&](const Tile &tile, int lo, int hi, int slot) {
+  walk<S::RT, S::KB, 0, S::WIN, S::WIN, D, kStreamThreads>(a, [&](const Tile &tile, int lo, int hi, int slot) {
     S::segment(a, L, tile, lo, hi, slot, gridDim.x);
   });
 }

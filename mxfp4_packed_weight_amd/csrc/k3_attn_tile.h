@@ -129,7 +129,7 @@ struct Tiled {
     int page[N];  // (all loads at once: the table has at least one entry)
 #pragma unroll
     for (int i = 0; i < N; i++)
-      page[i] = table[min(block_of(a, real_place<WIN, KB>(tile, x * KB + i * kThreads + threadIdx.x)),
+      page[i] = table[min(block_of(a, real_place<WIN>(tile, x * KB + i * kThreads + threadIdx.x)),
                           (uint32_t)a.blocks - 1)];
     [[maybe_unused]] uint64_t exps[N];
     if constexpr (BLK) {
@@ -142,7 +142,7 @@ struct Tiled {
     }
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      const int n = i * kThreads + threadIdx.x, y = x * KB + n, p = real_place<WIN, KB>(tile, y);
+      const int n = i * kThreads + threadIdx.x, y = x * KB + n, p = real_place<WIN>(tile, y);
       const int64_t row = y < end ? row_of(a, p, block_of(a, p), page[i]) : -1;
       L.row[at * KB + n] = row < 0 ? 0 : BLK ? (int64_t)((uint64_t)row | exps[i]) : row;
       const uint64_t there = __ballot(row >= 0);
@@ -269,10 +269,10 @@ struct Tiled {
   // their weights were, the sums are then no finite numbers either.
   static __device__ __forceinline__ void add_not_finite(const AttnArgs &a, f32x16 *o, const Tile &tile, int node,
                                                         const char *v, const int32_t *table, int y, int end, int h) {
-    const Request rq = without_gap<WIN, KB>(tile);
+    const Request rq = without_gap<WIN>(tile);
     const int near = WIN ? window_of(a, rq, node) : 0;
     for (; y < end; y++) {
-      const int p = real_place<WIN, KB>(tile, y);
+      const int p = real_place<WIN>(tile, y);
       const uint32_t b = block_of(a, p);
       const int64_t at = row_of(a, p, b, table[b]);
       if (at < 0 || !(seen(a, rq, node, y, 1) & 1)) continue;
@@ -468,7 +468,7 @@ struct Tiled {
                                                  int B) {
     const uint32_t lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Request shorter = without_gap<WIN, KB>(tile), &rq = WIN ? shorter : tile.q;
+    const Request shorter = without_gap<WIN>(tile), &rq = WIN ? shorter : tile.q;
     const int first_in_tile = 32 * (PAIRED ? wave >> 1 : wave), in_tile = first_in_tile + (int)c;
     const int rows = rq.n * a.G, first_row = tile.row0 + first_in_tile, row = tile.row0 + in_tile;
     const bool on = row < rows, any = first_row < rows;
@@ -650,7 +650,7 @@ template <bool BF, bool F8, int D, int MODE>
 __global__ __launch_bounds__(kAttnThreads<D>, kAttnWaves<D> / 4) void attn_tile_kernel(AttnArgs a) {
   using S = Tiled<BF, F8, D, MODE>;
   __shared__ typename S::Lds L;
-  walk<S::RT, S::KB, kPairedRows<D>, S::WIN, D, kAttnThreads<D>>(a, [&](const Tile &tile, int lo, int hi, int slot) {
+  walk<S::RT, S::KB, kPairedRows<D>, S::WIN, false, D, kAttnThreads<D>>(a, [&](const Tile &tile, int lo, int hi, int slot) {
     if constexpr (kPairedRows<D> > 0) {
       if (tile.rows <= kPairedRows<D>) return S::template segment<true>(a, L, tile, lo, hi, slot, gridDim.x);
     }

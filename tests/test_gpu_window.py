@@ -200,11 +200,13 @@ def test_strides_streams_and_graphs():
 
 
 def test_request_left_out():
-    """cu that is not ascending within [0, T]: those requests' rows stay as they were."""
-    import torch
+    """cu that is not ascending within [0, T]: those requests' rows stay as
+    they were; the others' are within the bound (how the work is cut depends on
+    the whole batch, so not to the bit)."""
     say("window with unsound cu")
     s = W.case([300, 200, 100], [4, 5, 3], 1, 4, 64, "bf16", "bf16", 16, 9, 64, 2)
-    want, _ = W.run(s)
+    want = [x[:4] for x in W.reference(s)]
     s["cu"] = np.array([0, 4, 10 ** 9, 12])
     got, lse = W.run(s)
-    assert torch.equal(got[:4], want[:4]) and (got[4:] == 7).all() and (lse[4:] == 7).all()
+    R_.check_attention(got[:4], lse[:4], want, "bf16", 304)
+    assert (got[4:] == 7).all() and (lse[4:] == 7).all()
