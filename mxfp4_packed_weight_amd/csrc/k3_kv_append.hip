@@ -2,14 +2,15 @@
 //
 //   e = ceil(log2(max |x| / 448)) over the page's new rows, not below that of
 //   rows that the page has already;  code = e4m3(x 2^-e)
-// A wave takes a page's new rows of one head, keys and values: it reads them
-// once, keeps them in registers while it finds the largest (pages of more than
-// kKeep loads are read again, out of the caches), and writes the codes. Only if
+// A wave, or two or four for a larger page, take a page's new rows of one head, keys and
+// values: they read them once, keep them in registers while they find the largest
+// (pages past that are read again, out of the caches), and write the codes. Only if
 // the exponent rises are the page's earlier codes read and rounded again. Which
 // page of which request follows without a prefix sum: n tokens touch at most
 // n / P + 2 pages, so that request r's are among the numbers from cu[r] / P + 2 r
 // on, and a search by 64 finds r.
 #include "k3_kv.h"
+#include "k3_lanes.h"
 #include "k3_rows.h"
 
 namespace k3 {
@@ -17,7 +18,7 @@ namespace k3 {
 namespace {
 
 constexpr int kAppendWaves = 4;
-constexpr int kKeep = 8;  // loads of a lane, keys and values alike
+constexpr int kKeep = 4;  // loads of a lane, keys and values alike
 
 // Eight values' largest size; infinities and NaN do not count.
 template <bool BF>
@@ -66,13 +67,15 @@ __device__ __forceinline__ uint2 lowered(uint2 w, int fall) {
   return to_e4m3(f);
 }
 
-template <bool BF, int D>
+// WAVES: of a page and head; more than one are a workgroup.
+template <bool BF, int D, int WAVES>
 __global__ __launch_bounds__(64 * kAppendWaves) void kv_append_kernel(KvAppendArgs a, int items) {
   constexpr int LPR = D / 8, RPL = 64 / LPR;  // lanes of a row, rows of a load
   const int lane = threadIdx.x & 63, sub = lane / LPR, d0 = lane % LPR * 8;
   const int H = a.c.n_heads, P = a.c.page_size;
   // (below 2^29: T / 4 and 2 R items, 2^10 heads)
-  const int unit = __builtin_amdgcn_readfirstlane(blockIdx.x * kAppendWaves + (threadIdx.x >> 6));
+  const int wave = threadIdx.x >> 6, part = WAVES == 1 ? 0 : wave;
+  const int unit = __builtin_amdgcn_readfirstlane(WAVES == 1 ? blockIdx.x * kAppendWaves + wave : blockIdx.x);
   const int item = unit / H, h = unit - item * H;
   if (item >= items) return;
   auto start = [&](int r) { return min(max(a.cu[r], 0), a.T) / P + 2 * r; };
@@ -92,48 +95,58 @@ __global__ __launch_bounds__(64 * kAppendWaves) void kv_append_kernel(KvAppendAr
   const int ctx = len - (int)n, j = item - (t0 / P + 2 * r), b = ctx / P + j;
   if (j < 0 || b > (len - 1) / P) return;
   const int page = a.table[(int64_t)r * a.blocks + b];
-  if (page < 0 || page >= a.c.n_pages) return;
   const int first = max(ctx, b * P), rows = min(len, b * P + P) - first, earlier = first - b * P;
   const int t = t0 + first - ctx;
   const uint16_t *in[2] = {a.k + t * a.k_stride + h * D + d0, a.v + t * a.v_stride + h * D + d0};
   const int64_t in_stride[2] = {a.k_stride, a.v_stride};
-  const int64_t at = page * a.c.page_stride + h * a.c.head_stride + d0;
-  uint8_t *out[2] = {(uint8_t *)a.c.k + at, (uint8_t *)a.c.v + at};
-  uint8_t *exps[2] = {a.k_exp + (int64_t)page * H + h, a.v_exp + (int64_t)page * H + h};
-
   uint4 x[2][kKeep];
   auto load = [&](int i0) {
 #pragma unroll
     for (int i = 0; i < kKeep; i++)
 #pragma unroll
       for (int s = 0; s < 2; s++) {
-        const int row = i0 + i * RPL + sub;
+        const int row = i0 + (part * kKeep + i) * RPL + sub;
         x[s][i] = uint4{0, 0, 0, 0};
         if (row < rows) x[s][i] = *(const uint4 *)(in[s] + row * in_stride[s]);
       }
   };
+  load(0);  // (on their way while the page is looked up)
+  if (page < 0 || page >= a.c.n_pages) return;
+  const int64_t at = page * a.c.page_stride + h * a.c.head_stride + d0;
+  uint8_t *out[2] = {(uint8_t *)a.c.k + at, (uint8_t *)a.c.v + at};
+  uint8_t *exps[2] = {a.k_exp + (int64_t)page * H + h, a.v_exp + (int64_t)page * H + h};
+
   int was[2] = {0, 0};  // the earlier rows' exponents
   if (earlier)
 #pragma unroll
     for (int s = 0; s < 2; s++) was[s] = min(max((int)*exps[s], 1), 254);
-  constexpr int CHUNK = kKeep * RPL;
+  constexpr int CHUNK = WAVES * kKeep * RPL;
   float top[2] = {0.f, 0.f};
   for (int i0 = 0; i0 < rows; i0 += CHUNK) {
-    load(i0);
+    if (i0) load(i0);
 #pragma unroll
     for (int i = 0; i < kKeep; i++)
 #pragma unroll
       for (int s = 0; s < 2; s++) top[s] = largest<BF>(x[s][i], top[s]);
   }
+#pragma unroll
+  for (int s = 0; s < 2; s++)
+    halving<32>([&](auto d) { top[s] = fmaxf(top[s], lane_xor<decltype(d)::value>(top[s])); });
+  if constexpr (WAVES > 1) {  // (they all come here: they have one page)
+    __shared__ float tops[WAVES][2];
+    if (lane < 2) tops[wave][lane] = lane ? top[1] : top[0];
+    __syncthreads();
+    for (int i = 0; i < WAVES; i++)
+#pragma unroll
+      for (int s = 0; s < 2; s++) top[s] = fmaxf(top[s], tops[i][s]);
+  }
   int byte[2];
 #pragma unroll
   for (int s = 0; s < 2; s++) {
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) top[s] = fmaxf(top[s], __shfl_xor(top[s], m));
     byte[s] = max(exponent_of(top[s]), was[s]);
-    if (lane == 0) *exps[s] = (uint8_t)byte[s];
+    if (lane == 0 && part == 0) *exps[s] = (uint8_t)byte[s];
     if (earlier && byte[s] > was[s])
-      for (int row = sub; row < earlier; row += RPL) {
+      for (int row = part * RPL + sub; row < earlier; row += WAVES * RPL) {
         uint2 *p = (uint2 *)(out[s] + row * a.c.slot_stride);
         *p = lowered(*p, byte[s] - was[s]);
       }
@@ -144,20 +157,31 @@ __global__ __launch_bounds__(64 * kAppendWaves) void kv_append_kernel(KvAppendAr
     for (int i = 0; i < kKeep; i++)
 #pragma unroll
       for (int s = 0; s < 2; s++) {
-        const int row = i0 + i * RPL + sub;
+        const int row = i0 + (part * kKeep + i) * RPL + sub;
         if (row < rows) *(uint2 *)(out[s] + (earlier + row) * a.c.slot_stride) = codes_of<BF>(x[s][i], byte[s]);
       }
   }
 }
 
+template <bool BF, int D>
+void launch(const KvAppendArgs &a, int items, hipStream_t s) {
+  const unsigned units = (unsigned)items * a.c.n_heads;
+  // A wave keeps kKeep loads of 512 / D rows. 16384 tokens of 8 heads of 128, pages
+  // of 16 / 32 / 64 places: 30 / 28 / 28 us; with one wave and eight loads 39 / 33 / 35.
+  const int most = kKeep * 512 / D, P = a.c.page_size;
+  if (P <= most)
+    kv_append_kernel<BF, D, 1><<<(units + kAppendWaves - 1) / kAppendWaves, 64 * kAppendWaves, 0, s>>>(a, items);
+  else if (P <= 2 * most) kv_append_kernel<BF, D, 2><<<units, 128, 0, s>>>(a, items);
+  else kv_append_kernel<BF, D, 4><<<units, 256, 0, s>>>(a, items);
+}
+
 template <bool BF>
 hipError_t by_dim(const KvAppendArgs &a, hipStream_t s) {
   const int items = a.T / a.c.page_size + 2 * a.R;
-  const unsigned grid = (unsigned)(((int64_t)items * a.c.n_heads + kAppendWaves - 1) / kAppendWaves);
   switch (a.c.head_dim) {
-    case 64: kv_append_kernel<BF, 64><<<grid, 64 * kAppendWaves, 0, s>>>(a, items); break;
-    case 128: kv_append_kernel<BF, 128><<<grid, 64 * kAppendWaves, 0, s>>>(a, items); break;
-    default: kv_append_kernel<BF, 256><<<grid, 64 * kAppendWaves, 0, s>>>(a, items);
+    case 64: launch<BF, 64>(a, items, s); break;
+    case 128: launch<BF, 128>(a, items, s); break;
+    default: launch<BF, 256>(a, items, s);
   }
   return hipGetLastError();
 }

@@ -8,6 +8,7 @@
 // is r times the largest |s w|, so that the row's sum of squares and a scale per
 // row need one exchange between the waves, and a group of up to 512 values is
 // in neighbouring lanes of a wave. The sum goes into the norm unrounded.
+#include "k3_lanes.h"
 #include "k3_rows.h"
 #include "k3_step.h"
 
@@ -16,9 +17,6 @@ namespace k3 {
 namespace {
 
 constexpr int kNormThreads = 1024, kNormWaves = kNormThreads / 64;
-
-// The larger of two, NaN if either is.
-__device__ __forceinline__ float larger(float a, float b) { return a > b || a != a ? a : b; }
 
 template <bool BF, bool QUANT, int VEC>
 __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) {
@@ -52,7 +50,7 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
       h[i][j] += r[j];
       ss = fmaf(h[i][j], h[i][j], ss);
       hw[i][j] = h[i][j] * w[j];
-      if (QUANT) top[i] = larger(fabsf(hw[i][j]), top[i]);
+      if (QUANT) top[i] = fmaxf(fabsf(hw[i][j]), top[i]);  // (NaN comes back with r)
     }
     if (a.sum && v < vectors) *(uint4 *)(a.sum + t * a.sum_stride + 8 * v) = pack8<BF>(h[i]);
   }
@@ -60,13 +58,13 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
   float most = 0.f;
   if (per_row) {
 #pragma unroll
-    for (int i = 0; i < VEC; i++) most = larger(top[i], most);
+    for (int i = 0; i < VEC; i++) most = fmaxf(top[i], most);
   }
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) {
-    ss += __shfl_xor(ss, m);
-    if (per_row) most = larger(most, __shfl_xor(most, m));
-  }
+  halving<32>([&](auto d) {
+    constexpr int M = decltype(d)::value;
+    ss += lane_xor<M>(ss);
+    if (QUANT) most = fmaxf(most, lane_xor<M>(most));
+  });
   if (lane == 0) {
     sums[wave] = ss;
     tops[wave] = most;
@@ -76,7 +74,7 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
   most = tops[0];
   for (int i = 1; i < waves; i++) {
     ss += sums[i];
-    most = larger(most, tops[i]);
+    most = fmaxf(most, tops[i]);
   }
   const float r = rsqrtf(ss / (float)a.hidden + a.eps);
   const int lanes = per_row ? 64 : a.group / 8;  // of a group
@@ -88,18 +86,22 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
     for (int j = 0; j < 8; j++) y[j] = hw[i][j] * r;
     if (a.y && v < vectors) *(uint4 *)(a.y + t * a.y_stride + 8 * v) = pack8<BF>(y);
     if (QUANT) {
-      float largest = per_row ? most : top[i];
-      if (!per_row)
-        for (int m = 1; m < lanes; m *= 2) largest = larger(largest, __shfl_xor(largest, m));
+      float largest = most;
+      if (!per_row) {  // over the group's lanes
+        largest = fmaxf(top[i], lane_xor<1>(top[i]));
+        largest = fmaxf(largest, lane_xor<2>(largest));
+        if (lanes >= 8) largest = fmaxf(largest, lane_xor<4>(largest));
+        if (lanes >= 16) largest = fmaxf(largest, lane_xor<8>(largest));
+        if (lanes >= 32) largest = fmaxf(largest, lane_xor<16>(largest));
+        if (lanes >= 64) largest = fmaxf(largest, lane_xor<32>(largest));
+      }
       if (v >= vectors) continue;
       float scale = largest * r * (1.f / 448.f);
       if (scale < 0x1p-126f) scale = 0.f;  // (not for NaN)
-      const float up = scale == 0.f ? 0.f : 1.f / scale;
+      // (at most 448 and four roundings, which is 448 in e4m3)
+      const float up = scale == 0.f ? 0.f : r / scale;
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const float q = y[j] * up;
-        y[j] = q != q ? q : fminf(fmaxf(q, -448.f), 448.f);
-      }
+      for (int j = 0; j < 8; j++) y[j] = hw[i][j] * up;
       *(uint2 *)(a.y8 + t * a.y8_stride + 8 * v) = to_e4m3(y);
       if (per_row ? v == 0 : v % lanes == 0) a.scales[t * (a.hidden / a.group) + v * 8 / a.group] = scale;
     }
