@@ -46,8 +46,11 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 // many places: its tables, queries and first blocks come one after the other
 // (14 us, at 1.8 us for 64 places of a head of 128).
 constexpr int kHalfCost = 11;
-template <int RT>
-constexpr int kFixedPlaces = RT < 128 ? 128 : 512;
+// (With a window, tiles of blocks of 256 places count three times as much: 64
+// single tokens over up to 8191 places with exponents 118 -> 110 us, 128 of them
+// 217 -> 199; 512 places are no better.)
+template <int RT, int KB, bool WIN>
+constexpr int kFixedPlaces = RT >= 128 ? 512 : WIN && KB >= 256 ? 384 : 128;
 constexpr int kMaxWorkgroups = 1024;  // of a launch: at most two to a CU
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The running maximum is raised only by more than this (in powers of two):
@@ -90,12 +93,12 @@ __device__ __forceinline__ int node_of(const AttnArgs &a, int row) {
 // 2^30 places keep all sums below 2^61.
 // With a window a tile has at most `cap`: tiles from `capped` on. unit: what a
 // tile counts if they go whole (0: they do not).
-template <int RT, int HALF, bool WIN>
+template <int RT, int KB, int HALF, bool WIN>
 struct Cost {
   int tiles, last_rows;
   long long base, slope, all;
   long long cap, capped, unit;  // WIN
-  static constexpr long long kFixed = 16 * kFixedPlaces<RT>;
+  static constexpr long long kFixed = 16 * kFixedPlaces<RT, KB, WIN>;
   __device__ __forceinline__ Cost(const AttnArgs &a, const Request &q, long long unit = 0) : unit(unit) {
     const long long rows = (long long)q.n * a.G;
     tiles = (int)((rows + RT - 1) / RT);
@@ -147,19 +150,19 @@ __device__ __forceinline__ int run_of(int R) { return (R + THREADS - 1) / THREAD
 // parts' way through memory and the joining launch). all: in sixteenths of a
 // place; most: the longest tile in places.
 constexpr int kUnit = 16;
-template <int RT>
+template <int RT, int KB>
 __device__ __forceinline__ long long unit_of(const AttnArgs &a, long long all, int tiles, int most) {
   const int rounds = (int)ceil((double)tiles * a.inv_groups);
-  return (double)rounds * most <= (double)all / 16 * a.inv_groups + 2 * kFixedPlaces<RT> ? kUnit : 0;
+  return (double)rounds * most <= (double)all / 16 * a.inv_groups + 2 * kFixedPlaces<RT, KB, true> ? kUnit : 0;
 }
-template <int RT, int HALF, bool WIN, int THREADS>
+template <int RT, int KB, int HALF, bool WIN, int THREADS>
 __device__ __forceinline__ long long line_of_tiles(const AttnArgs &a, Line<THREADS> &L) {
   const int tid = threadIdx.x, lane = tid & 63, per = run_of<THREADS>(a.R);
   long long own = 0;
   int own_tiles = 0, most = 0;  // (T * Hq <= 2^30 rows, 2^5 cost of a row at least)
   for (int r = tid * per; r < min(a.R, tid * per + per); r++) {
     const Request q = request_of(a, r);
-    const Cost<RT, HALF, WIN> cost(a, q);
+    const Cost<RT, KB, HALF, WIN> cost(a, q);
     own += cost.of_request(a);
     L.request[tid] = q;
     if constexpr (WIN) {
@@ -197,7 +200,7 @@ __device__ __forceinline__ long long line_of_tiles(const AttnArgs &a, Line<THREA
       all_tiles += L.wave_tiles[w];
       most = max(most, L.wave_most[w]);
     }
-    unit = unit_of<RT>(a, all, all_tiles, most);
+    unit = unit_of<RT, KB>(a, all, all_tiles, most);
     if (unit) {
       base = (long long)kUnit * before;
       own = (long long)kUnit * own_tiles;
@@ -264,7 +267,7 @@ __device__ __forceinline__ void fill_places(const AttnArgs &a, Tile &t) {
 }
 // The rest of a tile from q, r, h, x and first.
 template <int RT, int KB, int HALF, bool WIN>
-__device__ __forceinline__ void fill_tile(const AttnArgs &a, Tile &t, const Cost<RT, HALF, WIN> &cost) {
+__device__ __forceinline__ void fill_tile(const AttnArgs &a, Tile &t, const Cost<RT, KB, HALF, WIN> &cost) {
   t.tiles = cost.tiles;
   t.row0 = t.x * RT;
   t.rows = t.x == cost.tiles - 1 ? cost.last_rows : RT;
@@ -288,12 +291,12 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs &a, const Line<THREADS> &
   t.r = run * per;
   t.q = request_again(a, L, t.r);
   for (; t.r + 1 < min(a.R, run * per + per); t.r++) {
-    const long long all = Cost<RT, HALF, WIN>(a, t.q, unit).of_request(a);
+    const long long all = Cost<RT, KB, HALF, WIN>(a, t.q, unit).of_request(a);
     if (before + all > u) break;
     before += all;
     t.q = request_again(a, L, t.r + 1);
   }
-  const Cost<RT, HALF, WIN> cost(a, t.q, unit);
+  const Cost<RT, KB, HALF, WIN> cost(a, t.q, unit);
   // (the product is off by less than 1: n_heads <= 2^10)
   t.h = (int)((double)(u - before) * __builtin_amdgcn_rcp((double)cost.all));
   t.h = min(max(t.h, 0), a.c.n_heads - 1);
@@ -323,7 +326,7 @@ __device__ __forceinline__ void next_tile(const AttnArgs &a, const Line<THREADS>
       while (t.q.n == 0 && t.r + 1 < a.R);
     }
   }
-  fill_tile<RT, KB, HALF, WIN>(a, t, Cost<RT, HALF, WIN>(a, t.q, unit));
+  fill_tile<RT, KB, HALF, WIN>(a, t, Cost<RT, KB, HALF, WIN>(a, t.q, unit));
 }
 
 // The same in scalar registers: what was worked out in fp64 is in vector ones
@@ -338,12 +341,12 @@ __device__ __forceinline__ void to_scalars(Tile &t) {
 
 // The tile's first block that is done after place u of the line (any rising
 // function would do).
-template <int RT, int KB>
+template <int RT, int KB, bool WIN>
 __device__ __forceinline__ int block_from(const Tile &t, long long u) {
   if (u <= t.first) return 0;
   if (u >= t.after) return t.blocks;
   static_assert(kHalfCost == 11 && (KB & (KB - 1)) == 0, "");
-  long long y = max(u - t.first - 16 * kFixedPlaces<RT>, 0ll);
+  long long y = max(u - t.first - 16 * kFixedPlaces<RT, KB, WIN>, 0ll);
   if (t.weight != 16) y = y * 93 >> 6;  // 16 / 11
   return (int)min((y + 16 * KB - 1) / (16 * KB), (long long)t.blocks);
 }
@@ -354,7 +357,7 @@ __device__ __forceinline__ int block_from(const Tile &t, long long u) {
 // run: one place of one request 13.7 -> 11.1 us). Says whether they are.
 template <int RT, int KB>
 __device__ __forceinline__ long long short_cost(const Tile &t) {
-  return t.rows ? 16ll * (kFixedPlaces<RT> + t.places) : 0;
+  return t.rows ? 16ll * (kFixedPlaces<RT, KB, true> + t.places) : 0;
 }
 __device__ __forceinline__ void as_one_tile(const AttnArgs &a, Tile &t) {
   t.x = t.row0 = 0;
@@ -374,7 +377,7 @@ __device__ __forceinline__ bool short_line(const AttnArgs &a, Line<THREADS> &L, 
   const uint64_t here = __ballot(t.rows > 0);
   const long long own = short_cost<RT, KB>(t) * a.c.n_heads;
   long long incl = own;
-  int most = t.rows ? kFixedPlaces<RT> + t.places : 0;
+  int most = t.rows ? kFixedPlaces<RT, KB, true> + t.places : 0;
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) {
     const long long x = __shfl_up(incl, m);
@@ -400,7 +403,7 @@ __device__ __forceinline__ bool short_line(const AttnArgs &a, Line<THREADS> &L, 
     tiles += L.wave_tiles[w];
     most = max(most, L.wave_most[w]);
   }
-  unit = unit_of<RT>(a, all, tiles * a.c.n_heads, most);
+  unit = unit_of<RT, KB>(a, all, tiles * a.c.n_heads, most);
   if (unit) {
     base = (long long)(kUnit * a.c.n_heads) * before;
     all = (long long)(kUnit * a.c.n_heads) * tiles;
@@ -495,7 +498,7 @@ __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
   long long unit = 0;
   bool brief = false;
   if constexpr (SHORT) brief = a.R <= THREADS && short_line<RT, KB>(a, L, unit);
-  if (!brief) unit = line_of_tiles<RT, HALF, WIN, THREADS>(a, L);
+  if (!brief) unit = line_of_tiles<RT, KB, HALF, WIN, THREADS>(a, L);
   unit = WIN ? in_all_lanes(unit) : 0;
   const int B = gridDim.x, b = place_in_line(blockIdx.x, B);
   const Stretches line(a, in_all_lanes(L.pre[THREADS]), unit);
@@ -509,7 +512,7 @@ __device__ __forceinline__ void walk(const AttnArgs &a, Segment &&segment) {
     } else if (u == begin) tile = tile_at<RT, KB, HALF, WIN>(a, L, unit, u);
     else next_tile<RT, KB, HALF, WIN>(a, L, unit, tile);
     if constexpr (WIN) to_scalars(tile);
-    const int lo = block_from<RT, KB>(tile, u), hi = block_from<RT, KB>(tile, end);
+    const int lo = block_from<RT, KB, WIN>(tile, u), hi = block_from<RT, KB, WIN>(tile, end);
     const int slot = lo == hi || (lo == 0 && hi == tile.blocks) ? -1 : lo ? 2 * b : 2 * b + 1;
     if (u > tile.first) job.head_slot = slot;
     else if (tile.after > end) {
