@@ -152,6 +152,7 @@ __device__ __forceinline__ int run_of(int R) { return (R + THREADS - 1) / THREAD
 constexpr int kUnit = 16;
 template <int RT, int KB>
 __device__ __forceinline__ long long unit_of(const AttnArgs &a, long long all, int tiles, int most) {
+  if (a.whole) return kUnit;
   const int rounds = (int)ceil((double)tiles * a.inv_groups);
   return (double)rounds * most <= (double)all / 16 * a.inv_groups + 2 * kFixedPlaces<RT, KB, true> ? kUnit : 0;
 }

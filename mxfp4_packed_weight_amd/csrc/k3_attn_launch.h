@@ -9,6 +9,7 @@ namespace k3 {
 
 template <bool BF, int D>
 hipError_t launch_join(const AttnArgs &a, int B, hipStream_t s) {
+  if (a.whole) return hipGetLastError();
   if (const hipError_t e = hipGetLastError()) return e;
   attn_join_kernel<BF, D><<<join_workgroups(a, B), 64 * kJoinWaves, 0, s>>>(a, B);
   return hipGetLastError();

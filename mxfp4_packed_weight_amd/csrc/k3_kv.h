@@ -58,6 +58,7 @@ struct AttnArgs {
   int page_shift, group_shift;
   int window, sinks;  // a row at position x sees places below sinks, and above x - window (window >= 1)
   const uint8_t *k_exp, *v_exp;  // of pages and heads, or null
+  int whole;        // no tile is split, and nothing joined
   int slope;        // 16 tile_rows / G
   double inv_groups;  // 1 / workgroups of the launch
 };

@@ -61,6 +61,27 @@ int attn_workgroups(int tile_rows, int D) {
 
 static int attn_part_rows(int tile_rows, int T, int G) { return (int)std::min((long long)tile_rows, (long long)T * G); }
 
+// Whether a call with a window leaves all tiles whole, whatever its lengths are,
+// and needs no joining launch (about 4 us): if each has a workgroup of its own, and
+// the idle ones could not take more than so many places from it. Split / whole, us,
+// single tokens (of 16, 32, 64 requests, 8 key heads: 128, 256, 512 tiles for 512
+// workgroups), 8 query heads to a key head of 128, bf16:
+//   window   16 requests     32 requests     64 requests
+//   256      19.0 / 19.2     22.8 / 19.7     24.8 / 22.7
+//   512      23.7 / 25.5     28.8 / 27.1     33.7 / 30.7
+//   1024     29.7 / 39.7     39.4 / 42.1     51.7 / 49.2
+//   2048     37.9 / 67.6     56.2 / 72.4     87.7 / 84.8
+//   4096     50.7 / 122      81.4 / 131       143 / 150 (lengths differ)
+// and chunks of up to 2048 of 16 heads of 64 in windows of 1000 54.1 / 52.5.
+static bool attn_whole(const AttnArgs &a, int tile_rows, int D) {
+  // requests of n > 0 tokens have 1 + (n G - 1) / tile_rows tiles, and at most n each
+  const long long rows = (long long)a.T * a.G, k = std::min(a.R, a.T), each = (a.G + tile_rows - 1) / tile_rows;
+  const long long tiles = std::min(a.T * each, k + (rows - k) / tile_rows) * a.c.n_heads;
+  const long long places = (long long)a.window + a.sinks + (a.mask ? 32 * a.words : tile_rows / a.G);
+  const int B = attn_workgroups(tile_rows, D);
+  return tiles <= B && places <= 2200 && places * (B - tiles) <= 320ll * B;
+}
+
 size_t attn_workspace_bytes(int T, int Hq, int n_heads, int D) {
   // R is not known here: any tile up to the one request's may be taken
   const int G = Hq / n_heads, largest = attn_tile_rows(T, G, 1, D);
@@ -332,6 +353,7 @@ static k3_status attention(const char *fn, const void *q, int64_t q_stride, int 
   a.part_rows = attn_part_rows(tile_rows, T, a.G);
   a.slope = 16 * tile_rows / a.G;
   a.inv_groups = 1.0 / attn_workgroups(tile_rows, D);
+  a.whole = k_exp || window ? attn_whole(a, tile_rows, D) : 0;
   return device_status(launch_attention(a, k_exp ? kBlocks : window ? kWindow : kAllPlaces, stream), fn);
 }
 
