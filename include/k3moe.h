@@ -808,11 +808,12 @@ k3_status k3_block_attention(const void *q, int64_t q_stride, int dtype, int T,
  *   scales  fp32 [T][hidden / group], dense: max |y| / 448 over each `group`
  *           consecutive values; group is hidden (a scale per row), or 32, 64,
  *           128, 256 or 512 and divides it. A scale below 2^-126 is written
- *           as 0, with codes of 0. A group with a value that is not finite
- *           has a scale that is not finite.
+ *           as 0, with codes of 0. A group with a y that is not finite has a
+ *           scale that is not finite (weights are finite).
  * sum and y may be x or residual with that input's stride; otherwise the
  * outputs are apart from the inputs and from each other. Rows whose mean
- * square is past fp32's range give 0 (and NaN where s is infinite). */
+ * square is past fp32's range give 0 (and NaN where s is infinite); with eps = 0
+ * a row of zeros gives NaN. */
 k3_status k3_add_rms_norm(const void *x, int64_t x_stride, const void *residual,
                           int64_t residual_stride, int dtype, int T, int hidden,
                           const void *w, float eps, void *sum, int64_t sum_stride,

@@ -507,14 +507,15 @@ struct Tiled {
     for (int s = 0; s < NS; s++) w.q[s] ^= round;  // (only here are they waited for)
     // Begins turn j: fetches `rows` for a later one, and says where this one's
     // keys and values are, and the next one's.
-    auto begin = [&](int j, const Rows &rows, const lds_char *&now, lds_char *&next) {
+    // (used: the next one has keys or values; the first fetches' turns have none)
+    auto begin = [&](int j, bool used, const Rows &rows, const lds_char *&now, lds_char *&next) {
       now = buf + cur * kBuffer + half * ROW;
       if constexpr (F8) {
         fetch(rows, k, v, ring + raw * kRaw, lane, wave);
         raw = raw + 1 == kRaws ? 0 : raw + 1;
         cur = 1 - cur;
         next = buf + cur * kBuffer;
-        widen(L, ring + raw * kRaw, next, j + 1, lo);  // the oldest in the ring
+        if (used) widen(L, ring + raw * kRaw, next, j + 1, lo);  // the oldest in the ring
       } else {
         fetch(rows, k, v, buf + (cur == 0 ? kBuffers - 1 : cur - 1) * kBuffer, lane, wave);
         cur = cur + 1 == kBuffers ? 0 : cur + 1;
@@ -537,7 +538,7 @@ struct Tiled {
         const lds_char *now;
         lds_char *next;
         change_over<kInFlight>();
-        begin(j, rows, now, next);
+        begin(j, true, rows, now, next);
         rows = rows_after(L, rows, j + 1 + kAhead, lane, wave);
         if constexpr (!kPhases) {
           if (any) both<KT>(w, now, scale, lane);
@@ -567,7 +568,7 @@ struct Tiled {
         lds_char *next;
         change_over<kInFlight>();
         if ((j + kAhead) % (kListed / 2) == 0 && j + kAhead > lo) holes = list(a, L, tile, table, j + kAhead, end, holes);
-        begin(j, rows_of(L, j + kAhead, lo, lane, wave), now, next);
+        begin(j, !WIN || j + 1 >= lo, rows_of(L, j + kAhead, lo, lane, wave), now, next);
         if (j < lo) continue;
         if (j < hi && !whole(j)) {
           change_over<F8 ? 63 : NL>();

@@ -375,7 +375,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_logprobs_kernel(LogprobA
     list = x0 < 64 * kJoinWaves ? o : joined(list, o, lane);
   }
   for (int d = 1; d < used; d *= 2) {
-    if (wave & d) lists[wave][lane] = list;
+    if ((wave & (2 * d - 1)) == d) lists[wave][lane] = list;
     __syncthreads();
     if (!(wave & (2 * d - 1)) && wave + d < used) list = joined(list, lists[wave + d][lane], lane);
   }

@@ -176,3 +176,22 @@ def test_same_bits_on_a_stream_and_in_a_graph():
         torch.cuda.synchronize()
         for beta, o in zip((0.7, 1.0), outs):
             assert same(o, call(x, beta, tokens, k, ws=ws))
+
+
+def test_two_calls_at_once():
+    """On two streams, each with a workspace of its own."""
+    import torch
+    say("two calls of logprobs at once")
+    xs = [logits(2, 70001, "f32", 30), logits(5, 40000, "bf16", 31)]
+    tokens = [torch.arange(x.shape[0], dtype=torch.int32, device="cuda") for x in xs]
+    want = [call(x, 0.9, t, 20) for x, t in zip(xs, tokens)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for x, t, stream in zip(xs, tokens, streams):
+            with torch.cuda.stream(stream):
+                got.append(call(x, 0.9, t, 20))
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert all(torch.equal(o[n].view(torch.int32), want[i % 2][n].view(torch.int32)) for n in o), i

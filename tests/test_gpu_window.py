@@ -210,3 +210,24 @@ def test_request_left_out():
     got, lse = W.run(s)
     R_.check_attention(got[:4], lse[:4], want, "bf16", 304)
     assert (got[4:] == 7).all() and (lse[4:] == 7).all()
+
+
+def test_two_calls_at_once():
+    """On two streams, each with a workspace and outputs of its own: each has its own bits."""
+    import torch
+    say("two window calls at once")
+    cases = [W.case([3000, 40], [1, 30], 2, 4, 128, "bf16", "bf16", 16, 10, 900, 4),
+             W.case([800, 500, 60], [200, 1, 1], 2, 2, 64, "f16", "e4m3", 16, 11, 100, 1)]
+    want = [W.run(s) for s in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [torch.empty(K.k3_tree_attention_workspace_bytes(*s["q"].shape[:2], 2, s["q"].shape[2]), dtype=torch.uint8,
+                          device="cuda") for s in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for s, stream, ws in zip(cases, streams, spaces):
+            with torch.cuda.stream(stream):  # (inputs of the call are made on it as well)
+                got.append(W.call(s, ws=ws))
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[i % 2][0]) and torch.equal(lse, want[i % 2][1]), i
