@@ -138,7 +138,6 @@ struct Cost {
 template <int THREADS>
 struct Line {
   long long pre[THREADS + 1], wave_sum[THREADS / 64];
-  int wave_tiles[THREADS / 64], wave_most[THREADS / 64];  // WIN
   Request request[THREADS];  // the last of each thread's
 };
 template <int THREADS>
@@ -156,8 +155,13 @@ __device__ __forceinline__ long long unit_of(const AttnArgs &a, long long all, i
   const int rounds = (int)ceil((double)tiles * a.inv_groups);
   return (double)rounds * most <= (double)all / 16 * a.inv_groups + 2 * kFixedPlaces<RT, KB, true> ? kUnit : 0;
 }
+template <int THREADS>
+struct Counts {
+  int tiles[THREADS / 64], most[THREADS / 64];  // of the waves
+};
 template <int RT, int KB, int HALF, bool WIN, int THREADS>
 __device__ __forceinline__ long long line_of_tiles(const AttnArgs &a, Line<THREADS> &L) {
+  __shared__ Counts<WIN ? THREADS : 64> counts;
   const int tid = threadIdx.x, lane = tid & 63, per = run_of<THREADS>(a.R);
   long long own = 0;
   int own_tiles = 0, most = 0;  // (T * Hq <= 2^30 rows, 2^5 cost of a row at least)
@@ -186,8 +190,8 @@ __device__ __forceinline__ long long line_of_tiles(const AttnArgs &a, Line<THREA
   }
   if (lane == 63) L.wave_sum[tid >> 6] = incl;
   if (WIN && lane == 63) {
-    L.wave_tiles[tid >> 6] = tiles;
-    L.wave_most[tid >> 6] = most;
+    counts.tiles[tid >> 6] = tiles;
+    counts.most[tid >> 6] = most;
   }
   __syncthreads();
   long long base = incl - own, unit = 0;
@@ -197,9 +201,9 @@ __device__ __forceinline__ long long line_of_tiles(const AttnArgs &a, Line<THREA
     int all_tiles = 0, before = tiles - own_tiles;
     for (int w = 0; w < THREADS / 64; w++) {
       all += L.wave_sum[w];
-      if (w < (tid >> 6)) before += L.wave_tiles[w];
-      all_tiles += L.wave_tiles[w];
-      most = max(most, L.wave_most[w]);
+      if (w < (tid >> 6)) before += counts.tiles[w];
+      all_tiles += counts.tiles[w];
+      most = max(most, counts.most[w]);
     }
     unit = unit_of<RT, KB>(a, all, all_tiles, most);
     if (unit) {
@@ -368,6 +372,7 @@ __device__ __forceinline__ void as_one_tile(const AttnArgs &a, Tile &t) {
 }
 template <int RT, int KB, int THREADS>
 __device__ __forceinline__ bool short_line(const AttnArgs &a, Line<THREADS> &L, long long &unit) {
+  __shared__ Counts<THREADS> counts;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Tile t;
   t.q = {0, 0, 0};
@@ -388,8 +393,8 @@ __device__ __forceinline__ bool short_line(const AttnArgs &a, Line<THREADS> &L, 
   L.request[tid] = t.q;
   if (lane == 63) {
     L.wave_sum[wave] = incl;
-    L.wave_tiles[wave] = __popcll(here);
-    L.wave_most[wave] = most;
+    counts.tiles[wave] = __popcll(here);
+    counts.most[wave] = most;
   }
   if (!__syncthreads_and(one)) return false;
   long long all = 0, base = incl - own;
@@ -398,11 +403,11 @@ __device__ __forceinline__ bool short_line(const AttnArgs &a, Line<THREADS> &L, 
   for (int w = 0; w < THREADS / 64; w++) {
     if (w < wave) {
       base += L.wave_sum[w];
-      before += L.wave_tiles[w];
+      before += counts.tiles[w];
     }
     all += L.wave_sum[w];
-    tiles += L.wave_tiles[w];
-    most = max(most, L.wave_most[w]);
+    tiles += counts.tiles[w];
+    most = max(most, counts.most[w]);
   }
   unit = unit_of<RT, KB>(a, all, tiles * a.c.n_heads, most);
   if (unit) {
