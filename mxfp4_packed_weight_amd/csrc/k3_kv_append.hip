@@ -9,6 +9,10 @@
 // page of which request follows without a prefix sum: n tokens touch at most
 // n / P + 2 pages, so that request r's are among the numbers from cu[r] / P + 2 r
 // on, and a search by 64 finds r.
+//
+// 20480 tokens of 8 heads of 128 (126 MB): 29 us with warm rows, 34 without, 4.3
+// and 3.7 TB/s (a copy: 5.1); one token of each of 64 requests 5 us, four dependent
+// reads (lengths, table, exponents, codes), and 7 with its call on the host.
 #include "k3_kv.h"
 #include "k3_lanes.h"
 #include "k3_rows.h"
@@ -166,7 +170,7 @@ __global__ __launch_bounds__(64 * kAppendWaves) void kv_append_kernel(KvAppendAr
 template <bool BF, int D>
 void launch(const KvAppendArgs &a, int items, hipStream_t s) {
   const unsigned units = (unsigned)items * a.c.n_heads;
-  // A wave keeps kKeep loads of 512 / D rows. 16384 tokens of 8 heads of 128, pages
+  // A wave keeps kKeep loads of 512 / D rows. 20480 tokens of 8 heads of 128, pages
   // of 16 / 32 / 64 places: 30 / 28 / 28 us; with one wave and eight loads 39 / 33 / 35.
   const int most = kKeep * 512 / D, P = a.c.page_size;
   if (P <= most)
