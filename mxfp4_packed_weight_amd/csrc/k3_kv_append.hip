@@ -10,9 +10,11 @@
 // n / P + 2 pages, so that request r's are among the numbers from cu[r] / P + 2 r
 // on, and a search by 64 finds r.
 //
-// 20480 tokens of 8 heads of 128 (126 MB): 29 us with warm rows, 34 without, 4.3
-// and 3.7 TB/s (a copy: 5.1); one token of each of 64 requests 5 us, four dependent
-// reads (lengths, table, exponents, codes), and 7 with its call on the host.
+// 20480 tokens of 8 heads of 128 (126 MB): 24 us with warm rows, 5.2 TB/s (a copy:
+// 5.1); one token of each of 64 requests 5 us, four dependent reads (lengths,
+// table, exponents, codes), and 7 with its call on the host. Few instructions to a
+// value made that: sizes are compared two at a time as integers, and rows of
+// nothing but ordinary numbers take a way without checks (29 -> 24 us).
 #include "k3_kv.h"
 #include "k3_lanes.h"
 #include "k3_rows.h"
@@ -24,6 +26,23 @@ namespace {
 constexpr int kAppendWaves = 4;
 constexpr int kKeep = 4;  // loads of a lane, keys and values alike
 
+// The sizes of 16-bit numbers are in the order of their bits without the sign,
+// two to a word. Up to kUsual there is nothing but numbers whose codes are in range.
+template <bool BF>
+constexpr uint32_t kUsual = BF ? 0x7f7fu : 0x7b80u;  // bf16's largest; 61440
+__device__ __forceinline__ uint32_t larger_sizes(uint32_t x, uint32_t y) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, x), __builtin_bit_cast(u16x2, y)));
+}
+__device__ __forceinline__ uint32_t largest_bits(const uint4 &x, uint32_t top) {
+  constexpr uint32_t kSizes = 0x7fff7fffu;
+  return larger_sizes(larger_sizes(larger_sizes(larger_sizes(top, x.x & kSizes), x.y & kSizes), x.z & kSizes), x.w & kSizes);
+}
+template <bool BF>
+__device__ __forceinline__ float of_bits(uint32_t u) {
+  if (BF) return __builtin_bit_cast(float, u << 16);
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)u);
+}
 // Eight values' largest size; infinities and NaN do not count.
 template <bool BF>
 __device__ __forceinline__ float largest(const uint4 &x, float top) {
@@ -42,9 +61,15 @@ __device__ __forceinline__ int exponent_of(float amax) {
   return max((int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u), 1);
 }
 template <bool BF>
-__device__ __forceinline__ uint2 codes_of(const uint4 &x, int byte) {
+__device__ __forceinline__ uint2 codes_of(const uint4 &x, int byte, bool usual) {
   float f[8];
   unpack8<BF>(x, f);
+  if (usual) {
+    const float power = __builtin_bit_cast(float, (uint32_t)(254 - byte) << 23);  // (byte < 254)
+#pragma unroll
+    for (int j = 0; j < 8; j++) f[j] *= power;
+    return to_e4m3(f);
+  }
 #pragma unroll
   for (int j = 0; j < 8; j++) {
     // (fp16: 448 2^7 < 61440 = 240 2^8 < 65504, which would round to 2^16)
@@ -125,29 +150,54 @@ __global__ __launch_bounds__(64 * kAppendWaves) void kv_append_kernel(KvAppendAr
 #pragma unroll
     for (int s = 0; s < 2; s++) was[s] = min(max((int)*exps[s], 1), 254);
   constexpr int CHUNK = WAVES * kKeep * RPL;
-  float top[2] = {0.f, 0.f};
+  uint32_t bits[2] = {0, 0};
   for (int i0 = 0; i0 < rows; i0 += CHUNK) {
     if (i0) load(i0);
 #pragma unroll
     for (int i = 0; i < kKeep; i++)
 #pragma unroll
-      for (int s = 0; s < 2; s++) top[s] = largest<BF>(x[s][i], top[s]);
+      for (int s = 0; s < 2; s++) bits[s] = largest_bits(x[s][i], bits[s]);
   }
+  // the waves' largest: of bits, and of numbers where there are others among them
+  auto of_all = [&](uint32_t (&v)[2]) {
 #pragma unroll
-  for (int s = 0; s < 2; s++)
-    halving<32>([&](auto d) { top[s] = fmaxf(top[s], lane_xor<decltype(d)::value>(top[s])); });
-  if constexpr (WAVES > 1) {  // (they all come here: they have one page)
-    __shared__ float tops[WAVES][2];
-    if (lane < 2) tops[wave][lane] = lane ? top[1] : top[0];
-    __syncthreads();
-    for (int i = 0; i < WAVES; i++)
+    for (int s = 0; s < 2; s++)
+      halving<32>([&](auto d) { v[s] = max(v[s], lane_xor<decltype(d)::value>(v[s])); });
+    if constexpr (WAVES > 1) {  // (they all come here: they have one page)
+      __shared__ uint32_t tops[WAVES][2];
+      __syncthreads();
+      if (lane < 2) tops[wave][lane] = lane ? v[1] : v[0];
+      __syncthreads();
+      for (int i = 0; i < WAVES; i++)
 #pragma unroll
-      for (int s = 0; s < 2; s++) top[s] = fmaxf(top[s], tops[i][s]);
+        for (int s = 0; s < 2; s++) v[s] = max(v[s], tops[i][s]);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < 2; s++) bits[s] = max(bits[s] & 0xffffu, bits[s] >> 16);
+  of_all(bits);
+  float top[2] = {of_bits<BF>(bits[0]), of_bits<BF>(bits[1])};
+  bool usual = max(bits[0], bits[1]) <= kUsual<BF>;
+  if (!usual) {
+    float most[2] = {0.f, 0.f};
+    for (int i0 = 0; i0 < rows; i0 += CHUNK) {
+      if (rows > CHUNK) load(i0);
+#pragma unroll
+      for (int i = 0; i < kKeep; i++)
+#pragma unroll
+        for (int s = 0; s < 2; s++) most[s] = largest<BF>(x[s][i], most[s]);
+    }
+    // (numbers that are not negative are in the order of their bits)
+    uint32_t u[2] = {__builtin_bit_cast(uint32_t, most[0]), __builtin_bit_cast(uint32_t, most[1])};
+    of_all(u);
+    top[0] = __builtin_bit_cast(float, u[0]);
+    top[1] = __builtin_bit_cast(float, u[1]);
   }
   int byte[2];
 #pragma unroll
   for (int s = 0; s < 2; s++) {
     byte[s] = max(exponent_of(top[s]), was[s]);
+    usual &= byte[s] < 254;
     if (lane == 0 && part == 0) *exps[s] = (uint8_t)byte[s];
     if (earlier && byte[s] > was[s])
       for (int row = part * RPL + sub; row < earlier; row += WAVES * RPL) {
@@ -162,7 +212,7 @@ __global__ __launch_bounds__(64 * kAppendWaves) void kv_append_kernel(KvAppendAr
 #pragma unroll
       for (int s = 0; s < 2; s++) {
         const int row = i0 + (part * kKeep + i) * RPL + sub;
-        if (row < rows) *(uint2 *)(out[s] + (earlier + row) * a.c.slot_stride) = codes_of<BF>(x[s][i], byte[s]);
+        if (row < rows) *(uint2 *)(out[s] + (earlier + row) * a.c.slot_stride) = codes_of<BF>(x[s][i], byte[s], usual);
       }
   }
 }
@@ -171,7 +221,8 @@ template <bool BF, int D>
 void launch(const KvAppendArgs &a, int items, hipStream_t s) {
   const unsigned units = (unsigned)items * a.c.n_heads;
   // A wave keeps kKeep loads of 512 / D rows. 20480 tokens of 8 heads of 128, pages
-  // of 16 / 32 / 64 places: 30 / 28 / 28 us; with one wave and eight loads 39 / 33 / 35.
+  // of 16 / 32 / 64 places: 24 / 22 / 22 us (before the last step 30 / 28 / 28, and with
+  // one wave and eight loads 39 / 33 / 35).
   const int most = kKeep * 512 / D, P = a.c.page_size;
   if (P <= most)
     kv_append_kernel<BF, D, 1><<<(units + kAppendWaves - 1) / kAppendWaves, 64 * kAppendWaves, 0, s>>>(a, items);
