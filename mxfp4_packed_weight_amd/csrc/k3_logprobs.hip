@@ -1,11 +1,14 @@
 // Log probabilities of given tokens, entropy, and the largest logits of rows.
 //
-//   z = beta x,  lse = log sum exp z,  log p = z - lse,
-//   entropy = log S - Q / S,  S = sum e^d, Q = sum e^d d, d = z - beta m,
-// for a reference m that is at least near the largest of what was read so far:
-// one pass, S and Q are scaled when m rises. Differences are taken before the
-// factor beta, so that logits of the type's lowest value still differ by 0 from
-// one another. In e^d d an x of -inf counts as the lowest number, times 0.
+//   z = beta x / ln 2,  lse / ln 2 = log2 sum 2^z,  log2 p = z - log2 sum 2^z,
+//   entropy / ln 2 = log2 S - Q / S,  S = sum 2^d, Q = sum 2^d d,
+//   d = z - r for the reference r = z of m,
+// where m is at least near the largest of what was read so far: one pass, S and Q
+// are scaled when m rises. d is one fused operation, exact but for its own rounding
+// if r is taken as it was rounded. Where |r| reaches 2^20, so that what this
+// rounding leaves of z of m is no longer small, d is (x - m) beta / ln 2. In 2^d d a d of -inf counts as the lowest number, times 0; rows
+// without a list do that only in runs where the plain sum is not a number (16 bits:
+// 56 -> 51 us with the fused operation).
 //
 // A row's logits go to the waves in runs of 64 lanes x 16. Each wave keeps the
 // k <= 64 largest of its logits sorted in its lanes, one a lane. The logits of a
@@ -13,13 +16,13 @@
 // sorted and joined with the list: a comparison of one list with the other turned
 // round leaves the largest 64 of both, six steps of sorting order them. (Putting
 // them in one by one took four times as long: 64 rows of 131072 logits with 20
-// alternatives 41 -> 24 us.) Until a wave has k, a run's threshold is the k-th
+// alternatives 41 -> 24, now 21 us.) Until a wave has k, a run's threshold is the k-th
 // largest of its lanes' own maxima.
 //
 // 1000 rows of 150001 fp32 logits, 600 MB: 91 us, 6.6 TB/s (a plain read reaches
-// 7.1); with 20 alternatives 102 us. Rows of 16 bits are bound by the vector unit
-// (a dozen instructions to a logit, one of them an exponential at a quarter of the
-// rate): 56 us, 5.3 TB/s, 82 with 20 alternatives. One row of 131072: 11 us, two
+// 7.1); with 20 alternatives 103 us. Rows of 16 bits are bound by the vector unit
+// (ten instructions to a logit, one of them an exponential at a quarter of the
+// rate): 51 us, 5.9 TB/s, 80 with 20 alternatives. One row of 131072: 11 us, two
 // launches' latency. Runs further ahead than the next change nothing.
 #include <math.h>
 
@@ -64,12 +67,21 @@ __device__ __forceinline__ void unpack(const uint4 &p, float *f) {
 
 // ---- sums ---------------------------------------------------------------------
 
+constexpr float kPlain = 0x1p20f;
+// d of x for the reference m, r = m b2 rounded.
+__device__ __forceinline__ float above(float x, float m, float r, float b2) {
+  return fabsf(r) < kPlain ? fmaf(x, b2, -r) : (x - m) * b2;
+}
+
 struct Sums {
   float m, s, q;
-  // what is known of values below a higher reference, seen from it (x log2e beta = b2)
+  // what r's rounding left
+  static __device__ __forceinline__ float rest(float m, float b2) { return above(m, m, m * b2, b2); }
+  // what is known of values below a higher reference, seen from it (b2 = beta / ln 2)
   __device__ __forceinline__ void raise(float top, float b2) {
-    const float f = m == top ? 1.f : exp2f((m - top) * b2);
-    q = f == 0.f ? 0.f : f * (q - (top - m) * s);
+    const float fall = m == top ? 0.f : (m - top) * b2 + (rest(top, b2) - rest(m, b2));
+    const float f = exp2f(fall);
+    q = f == 0.f ? 0.f : f * (q + fall * s);
     s *= f;
     m = top;
   }
@@ -221,14 +233,38 @@ struct Wave {
       top = fmaxf(top, most[i]);
     }
     if (__ballot((top - sums.m) * b2 > 1.f)) sums.raise(fmaxf(sums.m, top), b2);
+    const float r = sums.m * b2;
+    if (!__ballot(!(fabsf(r) < kPlain))) {
+      float q = 0.f;
 #pragma unroll
-    for (int i = 0; i < LOADS; i++)
+      for (int i = 0; i < LOADS; i++)
 #pragma unroll
-      for (int j = 0; j < PER; j++) {
-        const float d = x[i][j] - sums.m, e = __builtin_amdgcn_exp2f(d * b2);
-        sums.s += e;
-        sums.q = fmaf(e, fmaxf(d, kLowest), sums.q);  // (0 times -inf is none)
+        for (int j = 0; j < PER; j++) {
+          const float d = fmaf(x[i][j], b2, -r), e = __builtin_amdgcn_exp2f(d);
+          sums.s += e;
+          q = fmaf(e, TOP ? fmaxf(d, kLowest) : d, q);
+        }
+      if (!TOP && __ballot(q != q)) {  // (0 times -inf is none; with a list there are no registers for this)
+        q = 0.f;
+#pragma unroll
+        for (int i = 0; i < LOADS; i++)
+#pragma unroll
+          for (int j = 0; j < PER; j++) {
+            const float d = fmaf(x[i][j], b2, -r);
+            q = fmaf(__builtin_amdgcn_exp2f(d), fmaxf(d, kLowest), q);
+          }
       }
+      sums.q += q;
+    } else {
+#pragma unroll
+      for (int i = 0; i < LOADS; i++)
+#pragma unroll
+        for (int j = 0; j < PER; j++) {
+          const float d = (x[i][j] - sums.m) * b2, e = __builtin_amdgcn_exp2f(d);
+          sums.s += e;
+          sums.q = fmaf(e, fmaxf(d, kLowest), sums.q);
+        }
+    }
     if (!TOP) return;
     if (last == -INFINITY) last = below_kth(top, k);  // (fewer than k so far)
     // (`last` stays as it is meanwhile: these are not in the order of their indices)
@@ -268,9 +304,12 @@ __device__ __forceinline__ float logit_of(const LogprobArgs &a, int t) {
 template <int TYPE>
 __device__ void finish(const LogprobArgs &a, int t, float logit, Sums sums, Entry list, int lane) {
   const char *row = (const char *)a.logits + t * a.stride * (16 / kPer<TYPE>);
-  const float log2_s = log2f(sums.s);
+  const float log2_s = log2f(sums.s), b2 = a.beta * kLog2e, r = sums.m * b2;
   auto log_p = [&](float x) {  // S = 0: no logit above -inf
-    return sums.s == 0.f ? -INFINITY : (x - sums.m) * a.beta - log2_s * kLn2;
+    if (sums.s == 0.f) return -INFINITY;
+    if (fabsf(x) >= 1e30f) return (x - sums.m) * a.beta - log2_s * kLn2;
+    const float p = (above(x, sums.m, r, b2) - log2_s) * kLn2;
+    return p > 0.f ? 0.f : p;  // (rounding)
   };
   if (lane == 0) {
     if (a.logprob) {
@@ -278,10 +317,10 @@ __device__ void finish(const LogprobArgs &a, int t, float logit, Sums sums, Entr
       a.logprob[t] = token >= 0 && token < a.V ? log_p(logit) : -INFINITY;
     }
     if (a.entropy) {
-      const float h = sums.s == 0.f ? 0.f : log2_s * kLn2 - a.beta * (sums.q / sums.s);
+      const float h = sums.s == 0.f ? 0.f : (log2_s - sums.q / sums.s) * kLn2;
       a.entropy[t] = h < 0.f ? 0.f : h;
     }
-    if (a.lse) a.lse[t] = sums.s == 0.f ? -INFINITY : fmaf(sums.m, a.beta, log2_s * kLn2);
+    if (a.lse) a.lse[t] = sums.s == 0.f ? -INFINITY : fmaf(sums.m, a.beta, (log2_s - Sums::rest(sums.m, b2)) * kLn2);
   }
   if (!a.k) return;
   float v = value_of(list);

@@ -109,6 +109,26 @@ def test_masked_rows(kind):
         check(x, 1.0, [200, 0, 300, 7, 6, 4000, V - 1, 4600], k)
 
 
+@pytest.mark.parametrize("k", [0, 7])
+@pytest.mark.parametrize("beta", [0.01, 1.0, 1.9])
+def test_large_numbers(beta, k):
+    """Logits about 1e30 and beyond, of both signs, alone and with ordinary ones, in one part and in several."""
+    import torch
+    say(f"logprobs of large numbers beta={beta} k={k}")
+    for T, V in ((6, 2003), (6, 70001)):
+        x = logits(T, V, "f32", 17, std=1.0).clone()
+        sizes = torch.tensor([0.9e30, 1e30, 1.1e30, 1e38], device="cuda")
+        big = sizes[(x.abs() * 1000).long() % 4]
+        x[0] = big[0].clamp(max=1.1e30)
+        x[1] = -big[1]
+        x[2, ::3] = -big[2, ::3]
+        x[3, V // 2:] = big[3, V // 2:]
+        x[4, :V - 2] = -big[4, :V - 2]
+        x[5] = -1e38
+        x[5, 1::2] = -math.inf
+        check(x, beta, [0, 1, 2, V - 1, V - 1, V // 2 | 1], k)
+
+
 def test_rows_of_no_numbers():
     """NaN and +inf: the row's figures are NaN, other rows' are not; NaN is not listed."""
     import torch
