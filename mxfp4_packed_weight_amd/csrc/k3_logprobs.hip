@@ -6,9 +6,11 @@
 // where m is at least near the largest of what was read so far: one pass, S and Q
 // are scaled when m rises. d is one fused operation, exact but for its own rounding
 // if r is taken as it was rounded. Where |r| reaches 2^20, so that what this
-// rounding leaves of z of m is no longer small, d is (x - m) beta / ln 2. In 2^d d a d of -inf counts as the lowest number, times 0; rows
-// without a list do that only in runs where the plain sum is not a number (16 bits:
-// 56 -> 51 us with the fused operation).
+// rounding leaves of z of m is no longer small, d is (x - m) beta / ln 2. In 2^d d
+// a d of -inf counts as the lowest number, times 0; rows without a list do that only
+// in runs where the plain sum is not a number (16 bits: 56 -> 51 us with the fused
+// operation). Lanes join by one change of reference each, to the largest of all, then
+// plain sums (51 -> 49; 64 rows with 20 alternatives 21 -> 18).
 //
 // A row's logits go to the waves in runs of 64 lanes x 16. Each wave keeps the
 // k <= 64 largest of its logits sorted in its lanes, one a lane. The logits of a
@@ -16,13 +18,13 @@
 // sorted and joined with the list: a comparison of one list with the other turned
 // round leaves the largest 64 of both, six steps of sorting order them. (Putting
 // them in one by one took four times as long: 64 rows of 131072 logits with 20
-// alternatives 41 -> 24, now 21 us.) Until a wave has k, a run's threshold is the k-th
+// alternatives 41 -> 24, now 18 us.) Until a wave has k, a run's threshold is the k-th
 // largest of its lanes' own maxima.
 //
-// 1000 rows of 150001 fp32 logits, 600 MB: 91 us, 6.6 TB/s (a plain read reaches
-// 7.1); with 20 alternatives 103 us. Rows of 16 bits are bound by the vector unit
+// 1000 rows of 150001 fp32 logits, 600 MB: 90 us, 6.7 TB/s (a plain read reaches
+// 7.1); with 20 alternatives 102 us. Rows of 16 bits are bound by the vector unit
 // (ten instructions to a logit, one of them an exponential at a quarter of the
-// rate): 51 us, 5.9 TB/s, 80 with 20 alternatives. One row of 131072: 11 us, two
+// rate): 49 us, 6.2 TB/s, 76 with 20 alternatives. One row of 131072: 11 us, two
 // launches' latency. Runs further ahead than the next change nothing.
 #include <math.h>
 
@@ -80,7 +82,7 @@ struct Sums {
   // what is known of values below a higher reference, seen from it (b2 = beta / ln 2)
   __device__ __forceinline__ void raise(float top, float b2) {
     const float fall = m == top ? 0.f : (m - top) * b2 + (rest(top, b2) - rest(m, b2));
-    const float f = exp2f(fall);
+    const float f = __builtin_amdgcn_exp2f(fall);
     q = f == 0.f ? 0.f : f * (q + fall * s);
     s *= f;
     m = top;
@@ -92,10 +94,15 @@ struct Sums {
     s += o.s;
     q += o.q;
   }
+  // of LANES lanes that follow one another, in each of them
+  template <int LANES = 64>
   __device__ __forceinline__ void join_lanes(float b2) {
-    halving<32>([&](auto d) {
-      constexpr int D = decltype(d)::value;
-      join(Sums{lane_xor<D>(m), lane_xor<D>(s), lane_xor<D>(q)}, b2);
+    float top = m;
+    halving<LANES / 2>([&](auto d) { top = fmaxf(top, lane_xor<decltype(d)::value>(top)); });
+    raise(top, b2);
+    halving<LANES / 2>([&](auto d) {
+      s += lane_xor<decltype(d)::value>(s);
+      q += lane_xor<decltype(d)::value>(q);
     });
   }
 };
@@ -382,10 +389,11 @@ __global__ __launch_bounds__(kThreads, 8) void token_logprobs_kernel(LogprobArgs
   }
   __syncthreads();
   if (wave) return;
+  w.sums = sums[lane % kWaves];
+  w.sums.template join_lanes<kWaves>(b2);
+  if (TOP) {
 #pragma unroll
-  for (int i = 1; i < kWaves; i++) {
-    w.sums.join(sums[i], b2);
-    if (TOP) w.list = joined(w.list, lists[i][lane], lane);
+    for (int i = 1; i < kWaves; i++) w.list = joined(w.list, lists[i][lane], lane);
   }
   if (a.parts == 1) return finish<TYPE>(a, t, logit, w.sums, w.list, lane);
   float *out = a.part + (int64_t)blockIdx.x * (4 + 2 * a.k);
