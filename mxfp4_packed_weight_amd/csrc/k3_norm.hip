@@ -103,10 +103,10 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
       if (v >= vectors) continue;
       float scale = largest * r * (1.f / 448.f);
       if (scale < 0x1p-126f) scale = 0.f;  // (not for NaN)
-      // (at most 448 and four roundings, which is 448 in e4m3)
-      const float up = scale == 0.f ? 0.f : r / scale;
+      // (at most 448 and four roundings, which is 448 in e4m3; r / scale may be infinite)
+      const float up = scale == 0.f ? 0.f : 1.f / scale;
 #pragma unroll
-      for (int j = 0; j < 8; j++) y[j] = hw[i][j] * up;
+      for (int j = 0; j < 8; j++) y[j] *= up;
       *(uint2 *)(a.y8 + t * a.y8_stride + 8 * v) = to_e4m3(y);
       if (per_row ? v == 0 : v % lanes == 0) a.scales[t * (a.hidden / a.group) + v * 8 / a.group] = scale;
     }

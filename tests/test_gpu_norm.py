@@ -118,6 +118,21 @@ def test_sizes_of_values(std):
     S.check_norm(o, *S.norm(x, None, w, 1e-6), "bf16", 128)
 
 
+@pytest.mark.parametrize("group", [128, 512])
+def test_small_rows_with_small_weights(group):
+    """No eps: the factor of the row over the scale is past fp32's range, the codes are not."""
+    import torch
+    say(f"norm of small rows with small weights group={group}")
+    T, N = 9, 512
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = ((1 + torch.rand((T, N), generator=g, device="cuda")) * 3e-19).bfloat16()
+    w = torch.full((N,), 1e-18, dtype=torch.bfloat16, device="cuda")
+    o = outputs(T, N, "bf16", True, group)
+    call(x, None, w, o, eps=0.0, group=group)
+    torch.cuda.synchronize()
+    S.check_norm(o, *S.norm(x, None, w, 0.0), "bf16", group)
+
+
 def test_another_stream_and_a_graph():
     """On a stream of its own, and replayed with other inputs."""
     import torch
