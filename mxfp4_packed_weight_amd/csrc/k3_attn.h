@@ -150,40 +150,40 @@ __device__ __forceinline__ int run_of(int R) { return (R + THREADS - 1) / THREAD
 // place; most: the longest tile in places.
 constexpr int kUnit = 16;
 template <int RT, int KB>
-__device__ __forceinline__ long long unit_of(const AttnArgs &a, long long all, int tiles, int most) {
+__device__ __forceinline__ long long unit_of(const AttnArgs &a, long long all, long long tiles, int most) {
   if (a.whole) return kUnit;
-  const int rounds = (int)ceil((double)tiles * a.inv_groups);
-  return (double)rounds * most <= (double)all / 16 * a.inv_groups + 2 * kFixedPlaces<RT, KB, true> ? kUnit : 0;
+  return ceil((double)tiles * a.inv_groups) * most <= (double)all / 16 * a.inv_groups + 2 * kFixedPlaces<RT, KB, true> ? kUnit : 0;
 }
 template <int THREADS>
 struct Counts {
-  int tiles[THREADS / 64], most[THREADS / 64];  // of the waves
+  long long tiles[THREADS / 64];  // of the waves
+  int most[THREADS / 64];
 };
 template <int RT, int KB, int HALF, bool WIN, int THREADS>
 __device__ __forceinline__ long long line_of_tiles(const AttnArgs &a, Line<THREADS> &L) {
   __shared__ Counts<WIN ? THREADS : 64> counts;
   const int tid = threadIdx.x, lane = tid & 63, per = run_of<THREADS>(a.R);
   long long own = 0;
-  int own_tiles = 0, most = 0;  // (T * Hq <= 2^30 rows, 2^5 cost of a row at least)
+  long long own_tiles = 0;  // (cu that goes back and forth counts rows many times)
+  int most = 0;
   for (int r = tid * per; r < min(a.R, tid * per + per); r++) {
     const Request q = request_of(a, r);
     const Cost<RT, KB, HALF, WIN> cost(a, q);
     own += cost.of_request(a);
     L.request[tid] = q;
     if constexpr (WIN) {
-      own_tiles += cost.tiles * a.c.n_heads;
+      own_tiles += (long long)cost.tiles * a.c.n_heads;
       const long long longest = cost.tiles ? max(cost.of(cost.tiles - 1), cost.of(max(cost.tiles - 2, 0))) : 0;
       most = max(most, (int)min(longest >> 4, (long long)INT32_MAX));
     }
   }
-  long long incl = own;
-  int tiles = own_tiles;
+  long long incl = own, tiles = own_tiles;
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) {
     const long long x = __shfl_up(incl, m);
     if (lane >= m) incl += x;
     if constexpr (WIN) {
-      const int t = __shfl_up(tiles, m);
+      const long long t = __shfl_up(tiles, m);
       if (lane >= m) tiles += t;
       most = max(most, __shfl_xor(most, m));
     }
@@ -197,8 +197,7 @@ __device__ __forceinline__ long long line_of_tiles(const AttnArgs &a, Line<THREA
   long long base = incl - own, unit = 0;
   for (int w = 0; w < (tid >> 6); w++) base += L.wave_sum[w];
   if constexpr (WIN) {
-    long long all = 0;
-    int all_tiles = 0, before = tiles - own_tiles;
+    long long all = 0, all_tiles = 0, before = tiles - own_tiles;
     for (int w = 0; w < THREADS / 64; w++) {
       all += L.wave_sum[w];
       if (w < (tid >> 6)) before += counts.tiles[w];
@@ -207,8 +206,8 @@ __device__ __forceinline__ long long line_of_tiles(const AttnArgs &a, Line<THREA
     }
     unit = unit_of<RT, KB>(a, all, all_tiles, most);
     if (unit) {
-      base = (long long)kUnit * before;
-      own = (long long)kUnit * own_tiles;
+      base = kUnit * before;
+      own = kUnit * own_tiles;
     }
   }
   L.pre[tid] = base;
