@@ -262,12 +262,12 @@ struct Wave {
           }
       }
       sums.q += q;
-    } else {
+    } else {  // (some lanes: those that have read nothing but -inf, for one, beside others with a reference of their own)
 #pragma unroll
       for (int i = 0; i < LOADS; i++)
 #pragma unroll
         for (int j = 0; j < PER; j++) {
-          const float d = (x[i][j] - sums.m) * b2, e = __builtin_amdgcn_exp2f(d);
+          const float d = above(x[i][j], sums.m, r, b2), e = __builtin_amdgcn_exp2f(d);
           sums.s += e;
           sums.q = fmaf(e, fmaxf(d, kLowest), sums.q);
         }
