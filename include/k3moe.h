@@ -836,9 +836,10 @@ k3_status k3_add_rms_norm(const void *x, int64_t x_stride, const void *residual,
  * A logit of -inf has p = 0, and is listed after all others; in a row of
  * nothing else every log p and lse are -inf, the entropy 0. A row with NaN or
  * +inf has NaN for all three; NaN logits are not listed, and places left over
- * have index -1 and NaN. Sums and differences are fp32. ws: at least
- * k3_token_logprobs_workspace_bytes(T, V, k) bytes (NULL if that is 0). The
- * same call gives the same bits. */
+ * have index -1 and NaN. Sums and differences are fp32. ws:
+ * k3_token_logprobs_workspace_bytes(T, V, k) bytes (NULL if that is 0) do for
+ * this call and for every one of at most as many rows, logits and k on the
+ * same device. The same call gives the same bits. */
 size_t k3_token_logprobs_workspace_bytes(int T, int V, int k);
 k3_status k3_token_logprobs(const void *logits, int64_t stride, int dtype, int T,
                             int V, float beta, const int32_t *tokens, int k,

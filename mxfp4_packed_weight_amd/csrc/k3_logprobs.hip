@@ -453,9 +453,14 @@ hipError_t launch(const LogprobArgs &a, hipStream_t s) {
 // logits with 20 alternatives take 102 us in one part (four to a CU), 113 in two,
 // 122 in four; one row of 131072, for which only latency counts, 10.7 us in 32
 // parts, 11.4 in 16 and 13.4 in 8.
-int logprob_parts(int T, int V) {
-  const int most = std::max(1, V / (kWaves * kRun));
-  return std::max(1, std::min(most, 4 * num_cus() / std::max(T, 1)));
+static int most_parts(int V) { return std::max(1, V / (kWaves * kRun)); }
+static int all_parts() { return 4 * num_cus(); }
+int logprob_parts(int T, int V) { return std::max(1, std::min(most_parts(V), all_parts() / std::max(T, 1))); }
+
+// Of several parts to a row no more than all_parts() are there, whatever T is:
+// as many as so many rows, or fewer, can have.
+size_t logprob_workspace_parts(int T, int V) {
+  return most_parts(V) == 1 ? 0 : std::min((size_t)T * most_parts(V), (size_t)all_parts());
 }
 
 hipError_t launch_token_logprobs(const LogprobArgs &a, hipStream_t s) {

@@ -31,6 +31,7 @@ struct LogprobArgs {
   int dtype, T, V, k, parts;
 };
 int logprob_parts(int T, int V);
+size_t logprob_workspace_parts(int T, int V);  // for up to T rows
 inline size_t logprob_part_words(int k) { return 4 + 2 * (size_t)k; }
 hipError_t launch_token_logprobs(const LogprobArgs &a, hipStream_t s);
 

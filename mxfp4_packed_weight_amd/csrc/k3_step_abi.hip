@@ -83,8 +83,7 @@ static k3_status check_logprobs(const char *fn, int T, int V, int k) {
 
 size_t k3_token_logprobs_workspace_bytes(int T, int V, int k) {
   if (check_logprobs("k3_token_logprobs_workspace_bytes", T, V, k) != K3_OK) return 0;
-  const size_t parts = logprob_parts(T, V);
-  return parts == 1 ? 0 : T * parts * logprob_part_words(k) * sizeof(float);
+  return logprob_workspace_parts(T, V) * logprob_part_words(k) * sizeof(float);
 }
 
 k3_status k3_token_logprobs(const void *logits, int64_t stride, int dtype, int T, int V, float beta,
@@ -107,8 +106,8 @@ k3_status k3_token_logprobs(const void *logits, int64_t stride, int dtype, int T
     KV_PTR(top, 4);
     KV_PTR(top_logprob, 4);
   }
-  const size_t need = k3_token_logprobs_workspace_bytes(T, V, k);
-  if (need) {
+  const size_t parts = logprob_parts(T, V), need = T * parts * logprob_part_words(k) * sizeof(float);
+  if (parts > 1) {
     KV_PTR(ws, 16);
     if (ws_bytes < need)
       return refuse(K3_ERR_MEMORY, "%s: workspace of %zu bytes is below the %zu bytes this call needs (give a larger "
@@ -129,7 +128,7 @@ k3_status k3_token_logprobs(const void *logits, int64_t stride, int dtype, int T
   a.T = T;
   a.V = V;
   a.k = k;
-  a.parts = logprob_parts(T, V);
+  a.parts = (int)parts;
   return device_status(launch_token_logprobs(a, stream), fn);
 }
 
