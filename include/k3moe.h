@@ -775,7 +775,11 @@ k3_status k3_window_attention(const void *q, int64_t q_stride, int dtype, int T,
  *
  * k3_block_attention is k3_window_attention without a mask over such a
  * cache: window = 0 for all places. Codes times their powers are exact in
- * bf16; in fp16 to 2^-25, and below 65520. k3_kv_commit moves codes without
+ * bf16 from 2^-126 on, in fp16 to 2^-25. Those from 2^128 (65520 for fp16
+ * queries) on count as infinities: in rows that see them, and in no others.
+ * (Of finite rows k3_kv_append makes such codes only of bf16 values from
+ * 248 * 2^120 on, which are rounded to 2^128; infinities next to them stay
+ * infinite.) k3_kv_commit moves codes without
  * their exponents: it is not for these caches. */
 k3_status k3_kv_append(const void *k_in, int64_t k_stride, const void *v_in,
                        int64_t v_stride, int dtype, int T, const k3_kv_cache *cache,

@@ -580,6 +580,21 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
   if ((w & (E << 16)) == (E << 16)) m |= 0xffff0000u;
   return m;
 }
+// Of a cache with exponents: whether a code times its power, in fp32 (exact), is
+// none of the finite numbers of the rows' type; with powers up to kSafePower no
+// code but NaN's is.
+template <bool BF>
+constexpr float kSafePower = BF ? 0x1p119f : 0x1p7f;  // 448 times it is below 2^128, 65504
+template <bool BF>
+__device__ __forceinline__ bool past_type(float x) {
+  return !(fabsf(x) < (BF ? INFINITY : 65520.f));
+}
+// The product if it is one of those, as the infinity or NaN it is in the type, else 0.
+template <bool BF>
+__device__ __forceinline__ float not_finite_product(uint32_t code, float power) {
+  const float x = __builtin_amdgcn_cvt_f32_fp8((int)code, 0) * power;
+  return past_type<BF>(x) ? x * INFINITY : 0.f;
+}
 template <bool BF>
 __device__ __forceinline__ float half_at(uint32_t w, int hi) {
   if (BF) return __builtin_bit_cast(float, hi ? w & 0xffff0000u : w << 16);

@@ -209,13 +209,22 @@ struct Stream {
     }
   }
 
-  // A word of V with its values that are not finite numbers set to zero.
-  static __device__ __forceinline__ uint32_t finite(uint32_t w) {
+  // A word of V with its values that are not finite numbers set to zero; power:
+  // of its place.
+  static __device__ __forceinline__ uint32_t finite(uint32_t w, float power) {
     if constexpr (F8) {
       uint32_t m = 0;  // 0x7f and 0xff are NaN; there is no infinity
 #pragma unroll
       for (int b = 0; b < 4; b++)
         if (((w >> (8 * b)) & 0x7f) == 0x7f) m |= 0xffu << (8 * b);
+      if constexpr (BLK) {
+        if (power > kSafePower<BF>) {  // (no code is infinite up to there)
+          if (past_type<BF>(__builtin_amdgcn_cvt_f32_fp8(w, 0) * power)) m |= 0xffu;
+          if (past_type<BF>(__builtin_amdgcn_cvt_f32_fp8(w, 1) * power)) m |= 0xff00u;
+          if (past_type<BF>(__builtin_amdgcn_cvt_f32_fp8(w, 2) * power)) m |= 0xff0000u;
+          if (past_type<BF>(__builtin_amdgcn_cvt_f32_fp8(w, 3) * power)) m |= 0xff000000u;
+        }
+      }
       return w & ~m;
     } else {
       return w & ~not_finite2<BF>(w);
@@ -225,8 +234,10 @@ struct Stream {
   // Places that some rows see and others do not, with values that are not
   // finite: those values' products with the weights of the rows that see
   // them (0 times NaN would reach the others). p holds q-tile t's weights.
+  // power: of the places.
   static __device__ __forceinline__ void add_not_finite(f32x4 *o, const float *p, uint32_t vis, const char *v,
-                                                     const int64_t *offset, float *scratch, int c, int g) {
+                                                     const int64_t *offset, const float *power, float *scratch, int c,
+                                                     int g) {
 #pragma unroll
     for (int j = 0; j < 8; j++) scratch[(16 * (j / 4) + 4 * g + j % 4) * 16 + c] = p[j];
     wave_sync();
@@ -242,7 +253,7 @@ struct Stream {
           float x;
           if (F8) {
             const uint32_t b = ((const uint8_t *)row)[d];
-            x = (b & 0x7f) == 0x7f ? NAN : 0.f;
+            x = BLK ? not_finite_product<BF>(b, power[key]) : (b & 0x7f) == 0x7f ? NAN : 0.f;
           } else {
             const uint32_t b = ((const uint16_t *)row)[d];
             x = not_finite2<BF>(b) & 0xffffu ? half_at<BF>(b, 0) : 0.f;
@@ -299,7 +310,7 @@ struct Stream {
         for (int j = 0; j < 8; j++)
 #pragma unroll
           for (int i = 0; i < VW; i++) {
-            const uint32_t f = finite(w.v[RUN][j][i]);
+            const uint32_t f = finite(w.v[RUN][j][i], v_power[j / 4]);
             lost |= f ^ w.v[RUN][j][i];
             w.v[RUN][j][i] = f;
           }
@@ -342,7 +353,7 @@ struct Stream {
       w.sum[t] += part;
 #pragma unroll
       for (int i = 0; i < 4; i++) p[t][i] = pack2<BF>(x[2 * i], x[2 * i + 1]);
-      if (odd) add_not_finite(w.o[t], x, vis, v, offset, scratch, c, g);
+      if (odd) add_not_finite(w.o[t], x, vis, v, offset, BLK ? power[1] + 32 * RUN : nullptr, scratch, c, g);
     }
 #pragma unroll
     for (int i = 0; i < VW; i++)

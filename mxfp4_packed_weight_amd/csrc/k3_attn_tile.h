@@ -283,13 +283,16 @@ struct Tiled {
       if (at < 0 || !(seen(a, rq, node, y, 1) & 1)) continue;
       if (WIN && !(in_window(a, near, y) & 1)) continue;
       const char *row = v + at;
+      const float power = BLK ? power_of(a.v_exp[(size_t)table[b] * a.c.n_heads + tile.h]) : 1.f;
 #pragma unroll
       for (int t = 0; t < DT; t++)
 #pragma unroll
         for (int i = 0; i < 16; i++) {
           const int d = 32 * t + 8 * (i / 4) + 4 * h + i % 4;
           float y;
-          if (F8) {
+          if (BLK) {
+            y = not_finite_product<BF>(((const uint8_t *)row)[d], power);
+          } else if (F8) {
             y = (((const uint8_t *)row)[d] & 0x7f) == 0x7f ? NAN : 0.f;
           } else {
             const uint32_t w = ((const uint16_t *)row)[d];
