@@ -102,9 +102,10 @@ __global__ __launch_bounds__(64 * kAppendWaves) void kv_append_kernel(KvAppendAr
   constexpr int LPR = D / 8, RPL = 64 / LPR;  // lanes of a row, rows of a load
   const int lane = threadIdx.x & 63, sub = lane / LPR, d0 = lane % LPR * 8;
   const int H = a.c.n_heads, P = a.c.page_size;
-  // (below 2^29: T / 4 and 2 R items, 2^10 heads)
+  // (below 2^29 in all: T / 4 and 2 R items, 2^10 heads)
   const int wave = threadIdx.x >> 6, part = WAVES == 1 ? 0 : wave;
-  const int unit = __builtin_amdgcn_readfirstlane(WAVES == 1 ? blockIdx.x * kAppendWaves + wave : blockIdx.x);
+  const int group = blockIdx.y * gridDim.x + blockIdx.x;
+  const int unit = __builtin_amdgcn_readfirstlane(WAVES == 1 ? group * kAppendWaves + wave : group);
   const int item = unit / H, h = unit - item * H;
   if (item >= items) return;
   auto start = [&](int r) { return min(max(a.cu[r], 0), a.T) / P + 2 * r; };
@@ -224,10 +225,15 @@ void launch(const KvAppendArgs &a, int items, hipStream_t s) {
   // of 16 / 32 / 64 places: 24 / 22 / 22 us (before the last step 30 / 28 / 28, and with
   // one wave and eight loads 39 / 33 / 35).
   const int most = kKeep * 512 / D, P = a.c.page_size;
+  // (2^32 threads do not fit into one dimension of a launch: 2^18 pages of 256 heads have them)
+  auto grid = [](unsigned groups) {
+    constexpr unsigned kRow = 1u << 23;
+    return dim3(groups < kRow ? groups : kRow, (groups + kRow - 1) / kRow);
+  };
   if (P <= most)
-    kv_append_kernel<BF, D, 1><<<(units + kAppendWaves - 1) / kAppendWaves, 64 * kAppendWaves, 0, s>>>(a, items);
-  else if (P <= 2 * most) kv_append_kernel<BF, D, 2><<<units, 128, 0, s>>>(a, items);
-  else kv_append_kernel<BF, D, 4><<<units, 256, 0, s>>>(a, items);
+    kv_append_kernel<BF, D, 1><<<grid((units + kAppendWaves - 1) / kAppendWaves), 64 * kAppendWaves, 0, s>>>(a, items);
+  else if (P <= 2 * most) kv_append_kernel<BF, D, 2><<<grid(units), 128, 0, s>>>(a, items);
+  else kv_append_kernel<BF, D, 4><<<grid(units), 256, 0, s>>>(a, items);
 }
 
 template <bool BF>
