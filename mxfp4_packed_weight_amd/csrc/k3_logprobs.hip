@@ -262,12 +262,15 @@ struct Wave {
           }
       }
       sums.q += q;
-    } else {  // (some lanes: those that have read nothing but -inf, for one, beside others with a reference of their own)
+    } else {
+      // some lanes' at least (those that have read nothing but -inf have the lowest number's): above(), lane by lane
+      const bool plain = fabsf(r) < kPlain;
+      const float from = plain ? 0.f : sums.m, less = plain ? r : 0.f;
 #pragma unroll
       for (int i = 0; i < LOADS; i++)
 #pragma unroll
         for (int j = 0; j < PER; j++) {
-          const float d = above(x[i][j], sums.m, r, b2), e = __builtin_amdgcn_exp2f(d);
+          const float d = fmaf(x[i][j] - from, b2, -less), e = __builtin_amdgcn_exp2f(d);
           sums.s += e;
           sums.q = fmaf(e, fmaxf(d, kLowest), sums.q);
         }
