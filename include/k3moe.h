@@ -817,8 +817,8 @@ k3_status k3_block_attention(const void *q, int64_t q_stride, int dtype, int T,
  * sum and y may be x or residual with that input's stride; otherwise the
  * outputs are apart from the inputs and from each other. Rows whose mean
  * square is past fp32's range give 0 (and NaN where s is infinite); with eps = 0
- * a row of zeros gives NaN. s * w is formed before the row's factor is known, and is
- * rounded as fp32 rounds it where it leaves the normal range. */
+ * a row of zeros gives NaN. Of other rows s * w is formed before the row's factor
+ * is known, and is rounded as fp32 rounds it where it leaves the normal range. */
 k3_status k3_add_rms_norm(const void *x, int64_t x_stride, const void *residual,
                           int64_t residual_stride, int dtype, int T, int hidden,
                           const void *w, float eps, void *sum, int64_t sum_stride,

@@ -7,7 +7,11 @@
 // stretches of it in registers: a row is read once. The largest |y| of a group
 // is r times the largest |s w|, so that the row's sum of squares and a scale per
 // row need one exchange between the waves, and a group of up to 512 values is
-// in neighbouring lanes of a wave. The sum goes into the norm unrounded.
+// in neighbouring lanes of a wave. The sum goes into the norm unrounded. Rows
+// whose squares leave fp32's range are summed once more, scaled: s stays in
+// registers for that, and s w is formed twice (2048 rows into e4m3 19.2 -> 19.5 us
+// with warm inputs; reading the inputs again instead takes more registers, and 4096
+// rows of 16384 88 -> 101 us).
 //
 // Bytes bound it: 16384 rows of 7168 with all three outputs, 1.06 GB: 180 us, 5.9
 // TB/s (a copy: 5.1); 2048 rows into e4m3 with scales of 128 values, 103 MB: 19 us
@@ -23,13 +27,23 @@ namespace {
 
 constexpr int kNormThreads = 1024, kNormWaves = kNormThreads / 64;
 
+// The largest |s w| of eight values.
+template <bool BF>
+__device__ __forceinline__ float largest_product(const float *s, const uint4 &weights) {
+  float w[8], top = 0.f;
+  unpack8<BF>(weights, w);
+#pragma unroll
+  for (int j = 0; j < 8; j++) top = fmaxf(fabsf(s[j] * w[j]), top);
+  return top;
+}
+
 template <bool BF, bool QUANT, int VEC>
 __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) {
   __shared__ float sums[kNormWaves], tops[kNormWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int64_t t = blockIdx.x;
   const int vectors = a.hidden / 8;
-  float h[VEC][8], hw[VEC][8];
+  float h[VEC][8];
   uint4 xs[VEC], rs[VEC], ws[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; i++) {
@@ -45,50 +59,98 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
 #pragma unroll
   for (int i = 0; i < VEC; i++) {
     const int v = i * blockDim.x + threadIdx.x;
-    float r[8], w[8];
+    float r[8];
     unpack8<BF>(xs[i], h[i]);
     unpack8<BF>(rs[i], r);
-    unpack8<BF>(ws[i], w);
     top[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
       h[i][j] += r[j];
       ss = fmaf(h[i][j], h[i][j], ss);
-      hw[i][j] = h[i][j] * w[j];
-      if (QUANT) top[i] = fmaxf(fabsf(hw[i][j]), top[i]);  // (NaN comes back with r)
     }
+    if (QUANT) top[i] = largest_product<BF>(h[i], ws[i]);  // (NaN comes back with r)
     if (a.sum && v < vectors) *(uint4 *)(a.sum + t * a.sum_stride + 8 * v) = pack8<BF>(h[i]);
   }
   const bool per_row = QUANT && a.group == a.hidden;
   float most = 0.f;
-  if (per_row) {
+  // the row's sum, and its largest if that is wanted, from each thread's
+  auto of_row = [&](float &sum) {
+    if (per_row) {
+      most = 0.f;
 #pragma unroll
-    for (int i = 0; i < VEC; i++) most = fmaxf(top[i], most);
+      for (int i = 0; i < VEC; i++) most = fmaxf(top[i], most);
+    }
+    halving<32>([&](auto d) {
+      constexpr int M = decltype(d)::value;
+      sum += lane_xor<M>(sum);
+      if (QUANT) most = fmaxf(most, lane_xor<M>(most));
+    });
+    if (lane == 0) {
+      sums[wave] = sum;
+      tops[wave] = most;
+    }
+    __syncthreads();
+    sum = sums[0];
+    most = tops[0];
+    for (int i = 1; i < waves; i++) {
+      sum += sums[i];
+      most = fmaxf(most, tops[i]);
+    }
+  };
+  of_row(ss);
+  const float mean = ss / (float)a.hidden + a.eps;
+  float r = rsqrtf(mean);
+  // The squares have left fp32's range where the rows may not have (fp16's cannot):
+  // again, of rows brought into its middle by a power of two (every thread has
+  // the same ss). A mean past the range makes r 0.
+  if (BF && (!(mean < INFINITY) || mean < 0x1p-100f) && ss == ss) {
+    const bool large = !(mean < INFINITY);
+    const float power = large ? 0x1p-80f : 0x1p80f;
+    float scaled = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; i++)
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const float x = h[i][j] * power;
+        scaled = fmaf(x, x, scaled);
+      }
+    __syncthreads();  // (the sums were read)
+    of_row(scaled);
+    scaled /= (float)a.hidden;
+    const bool past = large && !(scaled < 0x1p-32f), zero = !large && scaled + a.eps == 0.f;
+    const float factor = rsqrtf(scaled + a.eps * power * power);
+    if (!zero) {  // (else 0 times infinity, as it is)
+      r = past ? 0.f : 1.f;
+#pragma unroll
+      for (int i = 0; i < VEC; i++) {
+        if (QUANT && past) {
+          top[i] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; j++) top[i] = fmaxf(fabsf(h[i][j]), top[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          // (large: the power belongs to the factor, which it does not take out of range; small: to the value)
+          if (past) h[i][j] *= 0.f;
+          else h[i][j] = large ? h[i][j] * (factor * power) : h[i][j] * power * factor;
+        }
+        if (QUANT && !past) top[i] = largest_product<BF>(h[i], ws[i]);
+      }
+      if (per_row) {
+        float none = 0.f;
+        __syncthreads();
+        of_row(none);
+      }
+    }
   }
-  halving<32>([&](auto d) {
-    constexpr int M = decltype(d)::value;
-    ss += lane_xor<M>(ss);
-    if (QUANT) most = fmaxf(most, lane_xor<M>(most));
-  });
-  if (lane == 0) {
-    sums[wave] = ss;
-    tops[wave] = most;
-  }
-  __syncthreads();
-  ss = sums[0];
-  most = tops[0];
-  for (int i = 1; i < waves; i++) {
-    ss += sums[i];
-    most = fmaxf(most, tops[i]);
-  }
-  const float r = rsqrtf(ss / (float)a.hidden + a.eps);
   const int lanes = per_row ? 64 : a.group / 8;  // of a group
 #pragma unroll
   for (int i = 0; i < VEC; i++) {
     const int v = i * blockDim.x + threadIdx.x;
-    float y[8];
+    float y[8], w[8];
+    unpack8<BF>(ws[i], w);
 #pragma unroll
-    for (int j = 0; j < 8; j++) y[j] = hw[i][j] * r;
+    for (int j = 0; j < 8; j++) y[j] = h[i][j] * w[j] * r;
     if (a.y && v < vectors) *(uint4 *)(a.y + t * a.y_stride + 8 * v) = pack8<BF>(y);
     if (QUANT) {
       float largest = most;
