@@ -8,14 +8,13 @@
 // is r times the largest |s w|, so that the row's sum of squares and a scale per
 // row need one exchange between the waves, and a group of up to 512 values is
 // in neighbouring lanes of a wave. The sum goes into the norm unrounded. Rows
-// whose squares leave fp32's range are summed once more, scaled: s stays in
-// registers for that, and s w is formed twice (2048 rows into e4m3 19.2 -> 19.5 us
-// with warm inputs; reading the inputs again instead takes more registers, and 4096
-// rows of 16384 88 -> 101 us).
+// whose squares leave fp32's range are summed once more, scaled; s stays in registers
+// for that (reading the inputs again instead has to hold back the sum, which may go
+// over one of them: 4096 rows of 16384 88 -> 101 us).
 //
 // Bytes bound it: 16384 rows of 7168 with all three outputs, 1.06 GB: 180 us, 5.9
 // TB/s (a copy: 5.1); 2048 rows into e4m3 with scales of 128 values, 103 MB: 19 us
-// with warm inputs, 22 to 24 without. One row takes 2.4 us, and its call on the
+// with warm inputs, 22 without. One row takes 2.4 us, and its call on the
 // host three times that.
 #include "k3_lanes.h"
 #include "k3_rows.h"
@@ -27,13 +26,18 @@ namespace {
 
 constexpr int kNormThreads = 1024, kNormWaves = kNormThreads / 64;
 
-// The largest |s w| of eight values.
+// Eight values' products with their weights.
 template <bool BF>
-__device__ __forceinline__ float largest_product(const float *s, const uint4 &weights) {
-  float w[8], top = 0.f;
+__device__ __forceinline__ void weighted(const float *s, const uint4 &weights, float *out) {
+  float w[8];
   unpack8<BF>(weights, w);
 #pragma unroll
-  for (int j = 0; j < 8; j++) top = fmaxf(fabsf(s[j] * w[j]), top);
+  for (int j = 0; j < 8; j++) out[j] = s[j] * w[j];
+}
+__device__ __forceinline__ float largest_of(const float *x) {
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; j++) top = fmaxf(fabsf(x[j]), top);
   return top;
 }
 
@@ -43,7 +47,7 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int64_t t = blockIdx.x;
   const int vectors = a.hidden / 8;
-  float h[VEC][8];
+  float h[VEC][8], hw[VEC][8];
   uint4 xs[VEC], rs[VEC], ws[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; i++) {
@@ -62,13 +66,13 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
     float r[8];
     unpack8<BF>(xs[i], h[i]);
     unpack8<BF>(rs[i], r);
-    top[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
       h[i][j] += r[j];
       ss = fmaf(h[i][j], h[i][j], ss);
     }
-    if (QUANT) top[i] = largest_product<BF>(h[i], ws[i]);  // (NaN comes back with r)
+    weighted<BF>(h[i], ws[i], hw[i]);
+    top[i] = QUANT ? largest_of(hw[i]) : 0.f;  // (NaN comes back with r)
     if (a.sum && v < vectors) *(uint4 *)(a.sum + t * a.sum_stride + 8 * v) = pack8<BF>(h[i]);
   }
   const bool per_row = QUANT && a.group == a.hidden;
@@ -102,8 +106,10 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
   float r = rsqrtf(mean);
   // The squares have left fp32's range where the rows may not have (fp16's cannot):
   // again, of rows brought into its middle by a power of two (every thread has
-  // the same ss). A mean past the range makes r 0.
-  if (BF && (!(mean < INFINITY) || mean < 0x1p-100f) && ss == ss) {
+  // the same mean). A mean past the range makes r 0.
+  constexpr uint32_t kSmall = 0x0d800000u, kInf = 0x7f800000u;  // 2^-100, infinity
+  const uint32_t bits = __builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, mean));
+  if (BF && __builtin_expect(bits < kSmall || bits == kInf, 0)) {
     const bool large = !(mean < INFINITY);
     const float power = large ? 0x1p-80f : 0x1p80f;
     float scaled = 0.f;
@@ -123,18 +129,15 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
       r = past ? 0.f : 1.f;
 #pragma unroll
       for (int i = 0; i < VEC; i++) {
-        if (QUANT && past) {
-          top[i] = 0.f;
+        const int v = i * blockDim.x + threadIdx.x;
+        uint4 w = uint4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};  // (ones: 0 times s is 0 or NaN)
+        if (!past && v < vectors) w = *(const uint4 *)(a.w + 8 * v);
+        // (large: the power belongs to the factor, which it does not take out of range; small: to the value)
 #pragma unroll
-          for (int j = 0; j < 8; j++) top[i] = fmaxf(fabsf(h[i][j]), top[i]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-          // (large: the power belongs to the factor, which it does not take out of range; small: to the value)
-          if (past) h[i][j] *= 0.f;
-          else h[i][j] = large ? h[i][j] * (factor * power) : h[i][j] * power * factor;
-        }
-        if (QUANT && !past) top[i] = largest_product<BF>(h[i], ws[i]);
+        for (int j = 0; j < 8; j++)
+          if (!past) h[i][j] = large ? h[i][j] * (factor * power) : h[i][j] * power * factor;
+        weighted<BF>(h[i], w, hw[i]);
+        top[i] = QUANT ? largest_of(hw[i]) : 0.f;
       }
       if (per_row) {
         float none = 0.f;
@@ -143,14 +146,15 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
       }
     }
   }
-  const int lanes = per_row ? 64 : a.group / 8;  // of a group
+  // a group's lanes, and their logarithm (divisions by them took 0.7 us of 21.7, 2048
+  // rows into e4m3, whose bound is the vector unit as much as the bytes)
+  const int lanes = per_row ? 64 : a.group / 8, shift = per_row ? 31 : 31 - __builtin_clz(lanes | 1);
 #pragma unroll
   for (int i = 0; i < VEC; i++) {
     const int v = i * blockDim.x + threadIdx.x;
-    float y[8], w[8];
-    unpack8<BF>(ws[i], w);
+    float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) y[j] = h[i][j] * w[j] * r;
+    for (int j = 0; j < 8; j++) y[j] = hw[i][j] * r;
     if (a.y && v < vectors) *(uint4 *)(a.y + t * a.y_stride + 8 * v) = pack8<BF>(y);
     if (QUANT) {
       float largest = most;
@@ -170,7 +174,7 @@ __global__ __launch_bounds__(kNormThreads) void add_rms_norm_kernel(NormArgs a) 
 #pragma unroll
       for (int j = 0; j < 8; j++) y[j] *= up;
       *(uint2 *)(a.y8 + t * a.y8_stride + 8 * v) = to_e4m3(y);
-      if (per_row ? v == 0 : v % lanes == 0) a.scales[t * (a.hidden / a.group) + v * 8 / a.group] = scale;
+      if ((v & ((1u << shift) - 1)) == 0) a.scales[t * (per_row ? 1 : vectors >> shift) + (v >> shift)] = scale;
     }
   }
 }
