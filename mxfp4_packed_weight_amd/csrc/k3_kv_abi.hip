@@ -73,6 +73,17 @@ static int attn_part_rows(int tile_rows, int T, int G) { return (int)std::min((l
 //   2048     37.9 / 67.6     56.2 / 72.4     87.7 / 84.8
 //   4096     50.7 / 122      81.4 / 131       143 / 150 (lengths differ)
 // and chunks of up to 2048 of 16 heads of 64 in windows of 1000 54.1 / 52.5.
+// The bounds are of places, drawn for 16-bit rows of 128 values. Elsewhere a place
+// takes less time or more beside the launch; 16, 32 and 64 requests, split / whole:
+//   e4m3, 128      512    23.3 / 20.3  24.6 / 21.9  25.9 / 23.1
+//                  1024   25.0 / 28.2  32.7 / 30.0  35.4 / 32.5
+//                  2048   29.5 / 44.9  39.7 / 47.5  55.3 / 52.4
+//   bf16, 64       512    19.7 / 16.8  22.1 / 18.4  22.9 / 19.8
+//                  1024   22.6 / 25.2  27.0 / 26.5  32.4 / 29.7
+//   bf16, 4 of 256 512    29.7 / 28.8  32.7 / 30.0  35.9 / 33.6
+//                  1024   32.6 / 44.7  42.3 / 47.0  55.5 / 53.2
+// so that the rule takes the slower side by up to 3 us for 16 requests in windows of
+// 512 and, in e4m3, 32 in windows of 1024, and the faster one, or as good, in the others.
 static bool attn_whole(const AttnArgs &a, int tile_rows, int D) {
   // requests of n > 0 tokens have 1 + (n G - 1) / tile_rows tiles, and at most n each
   const long long rows = (long long)a.T * a.G, k = std::min(a.R, a.T), each = (a.G + tile_rows - 1) / tile_rows;

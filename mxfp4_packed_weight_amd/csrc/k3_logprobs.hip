@@ -22,10 +22,11 @@
 // largest of its lanes' own maxima.
 //
 // 1000 rows of 150001 fp32 logits, 600 MB: 90 us, 6.7 TB/s (a plain read reaches
-// 7.1); with 20 alternatives 102 us. Rows of 16 bits are bound by the vector unit
+// 7.1); with 20 alternatives 96 us. Rows of 16 bits are bound by the vector unit
 // (ten instructions to a logit, one of them an exponential at a quarter of the
-// rate): 49 us, 6.2 TB/s, 76 with 20 alternatives. One row of 131072: 11 us, two
-// launches' latency. Runs further ahead than the next change nothing.
+// rate): 51 us, 5.9 TB/s, 73 with 20 alternatives. One row of 131072: 10 to 11 us, two
+// launches' latency; 64 rows with 20 alternatives 18 us. Runs further ahead than the
+// next change nothing.
 #include <math.h>
 
 #include <algorithm>
@@ -453,9 +454,9 @@ hipError_t launch(const LogprobArgs &a, hipStream_t s) {
 // Parts of a row: so many that four workgroups are there for each CU, and each
 // wave of a part has a run. Every wave has a list of its own to begin and to
 // join, so that more of them cost more than they hide: 1000 rows of 150001 fp32
-// logits with 20 alternatives take 102 us in one part (four to a CU), 113 in two,
-// 122 in four; one row of 131072, for which only latency counts, 10.7 us in 32
-// parts, 11.4 in 16 and 13.4 in 8.
+// logits with 20 alternatives take 97 us in one part (four to a CU), 104 in two,
+// 110 in four; one row of 131072, for which only latency counts, 11.5 us in 32
+// parts, 11.9 in 16 and 13.5 in 8 (with the calls' time on the host).
 static int most_parts(int V) { return std::max(1, V / (kWaves * kRun)); }
 static int all_parts() { return 4 * num_cus(); }
 int logprob_parts(int T, int V) { return std::max(1, std::min(most_parts(V), all_parts() / std::max(T, 1))); }
