@@ -761,7 +761,7 @@ k3_status k3_window_attention(const void *q, int64_t q_stride, int dtype, int T,
  * k3_kv_append appends a step's rows: token cu[r] + i of request r goes to
  * the place kv_lens[r] - n + i, n = cu[r + 1] - cu[r]. A page's exponent for
  * a head becomes the smallest 2^e with max |x| <= 448 2^e over the new rows
- * that go there (1 if all are 0), or stays where the page holds earlier rows
+ * that go there (byte 1 if all are 0), or stays where the page holds earlier rows
  * (places below kv_lens[r] - n) whose exponent is larger; if it rises, those
  * rows' codes are rounded to the new one (only codes that leave e4m3's normal
  * range lose anything). Rows are rounded once, to nearest even. NaN stays
@@ -779,8 +779,8 @@ k3_status k3_window_attention(const void *q, int64_t q_stride, int dtype, int T,
  * queries) on count as infinities: in rows that see them, and in no others.
  * (Of finite rows k3_kv_append makes such codes only of bf16 values from
  * 248 * 2^120 on, which are rounded to 2^128; infinities next to them stay
- * infinite.) k3_kv_commit moves codes without
- * their exponents: it is not for these caches. */
+ * infinite.) k3_kv_commit moves codes without their exponents: it is not for
+ * these caches. */
 k3_status k3_kv_append(const void *k_in, int64_t k_stride, const void *v_in,
                        int64_t v_stride, int dtype, int T, const k3_kv_cache *cache,
                        uint8_t *k_exp, uint8_t *v_exp, const int32_t *table,
